@@ -195,8 +195,8 @@ typedef struct qdg_std_weights {
 
 typedef struct qdg_plan qdg_plan;
 
-/* Input flags: bits that qdg_preprocess and qdg_moe_align OR into an
-   optional caller-owned device status word (uint32_t, 4-byte aligned) when
+/* Input flags: bits that qdg_preprocess, qdg_moe_align and
+   qdg_moe_route OR into an optional caller-owned device status word (uint32_t, 4-byte aligned) when
    they meet input the standard format does not allow. The call still
    completes and its outputs are defined (noted per flag); a caller that
    passes the word zeroes it beforehand and reads it after the stream has
@@ -214,9 +214,13 @@ enum {
                                     non-finite f16 / f32 scale is packed as it is */
   QDG_FLAG_BAD_ZERO_POINT = 2u,  /* a UINT4 zero point above 15 (UINT2:
                                     above 3); packed modulo 128 */
-  QDG_FLAG_BAD_EXPERT_ID = 4u    /* a top-k id outside [0, E); the pair is
+  QDG_FLAG_BAD_EXPERT_ID = 4u,   /* a top-k id outside [0, E); the pair is
                                     left out of every expert block, so its
                                     output row is never written */
+  QDG_FLAG_BAD_LOGIT = 8u        /* qdg_moe_route: a NaN logit or bias (the
+                                    expert is masked for that token) or a
+                                    logit of +infinity (taken as the largest
+                                    finite binary32) */
 };
 
 /* Library identity: "qdg <version> gfx950 layout <QDG_LAYOUT_VERSION>". */
@@ -509,6 +513,128 @@ qdg_status qdg_moe_combine(const float* y, const float* w, int64_t T, int32_t to
    Arguments, alignment of w and out, and errors as for qdg_moe_combine. */
 qdg_status qdg_moe_combine_bf16(const void* y, const float* w, int64_t T, int32_t top_k, int64_t n, void* out,
                                 int32_t otype, void* stream);
+
+/* ---------------------------------------------------------------- routing
+   Expert routing: the step in front of qdg_moe_align (each token activates a
+   few of the stored experts: kinachrichten, "Warum quantisierte Kernel
+   wichtig sind"; the pages fix no routing rule, the rules below are this
+   library's reading). For each token, over its E logits l:
+     score   s_e = exp(l_e) / sum_f exp(l_f)  (SOFTMAX)  or
+             s_e = 1 / (1 + exp(-l_e))        (SIGMOID)
+     key     c_e = s_e + bias_e (a correction for balance: it decides which
+             experts are taken, never their weights); without a bias the
+             experts are ordered by their logits, in which s_e increases
+     groups  num_groups > 1: the E experts are num_groups equal runs; a
+             group's value is its largest c (MAX) or the sum of its two
+             largest (TOP2; without a bias c = s here); the topk_groups groups
+             with the largest values stay, equal ones the lower index first
+     choice  the top_k experts of the groups that stay with the largest keys,
+             in descending order, equal ones the lower index first
+     weight  w = s_e of the chosen, with renormalize divided by their sum
+             (0 where the sum is 0), times scale
+   Keys and group values decide as in binary64 (a choice between two that
+   binary32 cannot tell apart is not left to its rounding); the weights are
+   within 2^-21 of their exact values (relative).
+   Masked experts: a logit of -infinity or NaN, or a bias of -infinity or
+   NaN, masks an expert: its score is 0, it ranks behind every expert that
+   is not masked and adds nothing to a group's value (a group of masked
+   experts ranks last). Where fewer than top_k others are left, the lowest
+   masked experts of the groups that stay fill the remaining slots with
+   weight 0, so that every id is valid for qdg_moe_align.
+   num_experts 1..1024; top_k 1..32 and at most topk_groups * (num_experts /
+   num_groups); num_groups 0 or 1 (none) or up to 64, dividing num_experts;
+   1 <= topk_groups <= num_groups; scale finite. */
+enum { QDG_L_BF16 = 0, QDG_L_F16 = 1, QDG_L_F32 = 2 };          /* logit types */
+enum { QDG_SCORE_SOFTMAX = 0, QDG_SCORE_SIGMOID = 1 };
+enum { QDG_GROUP_MAX = 0, QDG_GROUP_TOP2 = 1 };
+typedef struct qdg_route_config {
+  int32_t num_experts, top_k;
+  int32_t ltype, score;
+  int32_t num_groups, topk_groups, group_score;
+  int32_t renormalize;
+  float scale;
+} qdg_route_config;
+
+/* logits [T][num_experts] of ltype, row stride ld elements (>= num_experts);
+   bias f32 [num_experts] or NULL; topk_ids i32 [T][top_k] and topk_weights
+   f32 [T][top_k], contiguous. `status` (may be NULL; device, 4-byte aligned,
+   caller-owned and caller-zeroed) receives QDG_FLAG_BAD_LOGIT. T >= 0 (0
+   enqueues nothing). Device pointers aligned to their elements. One launch,
+   no workspace. Errors: QDG_ERR_INVALID_ARG (NULL pointers, T < 0, a config
+   value out of its range), QDG_ERR_UNSUPPORTED (more than 1024 experts, 64
+   groups or top_k 32, T >= 2^31), QDG_ERR_MISALIGNED. */
+qdg_status qdg_moe_route(const qdg_route_config* cfg, const void* logits, int64_t ld, const float* bias, int64_t T,
+                         int32_t* topk_ids, float* topk_weights, uint32_t* status, void* stream);
+
+/* ------------------------------------- int8 products over stored operands
+   The W8A8 product over row-major operands as they are stored: no
+   qdg_preprocess, any n and k, row strides, a zero point for each token, a
+   bias, and the SiLU*mul epilogue for dense layers too. For weights that
+   change between calls, for operands that are views, and for activations
+   that lie on one side of zero (asymmetric codes spend all 256 on them).
+
+   Asymmetric activation quantizer: per token, over the finite values of its
+   row, lo = min(0, min x), hi = max(0, max x);
+     scale = f32((hi - lo) / 255), at least 2^-126;  1 if hi = lo
+     zero  = clamp(rne(-128 - lo * inv), -128, 127); 0 if hi = lo
+     code  = clamp(rne(x * inv) + zero, -128, 127),  inv = 1 / scale
+   with inv and the products in binary64, so the codes are reproducible bit
+   for bit; x ~ (code - zero) * scale, and 0 is exact. +-infinity takes the
+   end codes, NaN the code of 0.
+   a_bf16 [M][k], row stride lda elements (a multiple of 8, >= k); qa i8
+   [M][k], row stride ldq bytes (a multiple of 16, >= k; bytes behind k stay
+   as they were); a_scales f32 [M]; a_zeros i32 [M]. a_bf16 and qa 16-byte
+   aligned, the others 4-byte. M >= 0 (0 enqueues nothing), k >= 1. Errors:
+   QDG_ERR_INVALID_ARG, QDG_ERR_MISALIGNED, QDG_ERR_UNSUPPORTED (M >= 2^31 or
+   k > 2^30). */
+qdg_status qdg_quantize_act_zp(const void* a_bf16, int64_t lda, int64_t M, int64_t k, int8_t* qa, int64_t ldq,
+                               float* a_scales, int32_t* a_zeros, void* stream);
+
+/* A layer of the direct int8 product. B i8 [num_experts][n][k], rows of ldb
+   bytes, experts n * ldb bytes apart; lda and ldb multiples of 16, >= k; Y
+   rows of ldy elements, >= its columns (n, or n / 2 with QDG_EPI_SILU_MUL).
+   otype BF16, F32, or I32 (the exact integers; scales and bias are ignored
+   and may be NULL; not with an epilogue). epilogue QDG_EPI_NONE or
+   QDG_EPI_SILU_MUL (n even: rows [0, n/2) of B the gate, [n/2, n) the up
+   projection; any n / 2). n in [1, 2^26], k in [1, 65536] (so that the sums
+   over (qa - za) * qb, at most 255 * 128 each, stay within int32),
+   num_experts 1..1024. */
+typedef struct qdg_i8_config {
+  int64_t n, k;
+  int64_t lda, ldb, ldy;
+  int32_t num_experts, otype, epilogue, reserved; /* reserved: 0 */
+} qdg_i8_config;
+
+/* Workspace bytes qdg_gemm_i8 needs for M rows (0: none; int32 partials of a
+   product whose K is split over workgroups, added by a second kernel). Its
+   contents need no initialisation. Calls that share a workspace must be
+   ordered on one stream. */
+qdg_status qdg_gemm_i8_workspace(const qdg_i8_config* cfg, int64_t M, size_t* bytes);
+
+/* Y[m][j] = a_scales[m] * b_scales[j] * sum_k (A[m][k] - a_zeros[m]) * B[j][k]
+   + bias[j], the sum exact in int32, then the epilogue and one rounding to
+   otype. cfg->num_experts = 1. a_scales f32 [M]; a_zeros i32 [M], values in
+   [-128, 127], or NULL (all 0); b_scales f32 [n]; bias f32 [n] or NULL. A and
+   B 16-byte aligned, the others aligned to their elements; workspace 16-byte
+   aligned, NULL where none is needed. Bytes of A and B rows behind k may hold
+   anything. M in [0, 2^26] (0 enqueues nothing). Row m of Y does not depend
+   on M or on the other rows, and results are the same on every call. */
+qdg_status qdg_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const float* a_scales, const int32_t* a_zeros,
+                       const int8_t* B, const float* b_scales, const float* bias, void* Y, int64_t M,
+                       void* workspace, size_t ws_bytes, void* stream);
+
+/* The same product grouped by expert over the routing arrays of
+   qdg_moe_align(T, top_k, cfg->num_experts, block_m): for every real entry i
+   of sorted_ids in block b, row i of Y [T*top_k][columns] is A row r with
+   the operands of expert block_expert[b], r = i (a_per_pair = 1) or
+   i / top_k (a_per_pair = 0). a_scales and a_zeros are indexed by r,
+   b_scales and bias are f32 [num_experts][n]. Rows without a real entry stay
+   as they were. block_m in {16, 32, 64, 128}: the smaller while experts hold
+   few rows each. T*top_k <= 2^20. No workspace. */
+qdg_status qdg_moe_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const float* a_scales, const int32_t* a_zeros,
+                           const int8_t* B, const float* b_scales, const float* bias, const int32_t* sorted_ids,
+                           const int32_t* block_expert, const int32_t* num_padded, int64_t T, int32_t top_k,
+                           int32_t block_m, int32_t a_per_pair, void* Y, void* stream);
 
 #ifdef __cplusplus
 }

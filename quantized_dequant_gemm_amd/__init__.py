@@ -25,7 +25,10 @@ QDG_A_BF16, QDG_A_INT8, QDG_A_FP8E4M3, QDG_A_MXFP4 = range(4)
 QDG_O_BF16, QDG_O_F32, QDG_O_I32 = range(3)
 QDG_KIND_DENSE, QDG_KIND_MOE = range(2)
 QDG_EPI_NONE, QDG_EPI_SILU_MUL = range(2)
-QDG_FLAG_BAD_SCALE, QDG_FLAG_BAD_ZERO_POINT, QDG_FLAG_BAD_EXPERT_ID = 1, 2, 4
+QDG_FLAG_BAD_SCALE, QDG_FLAG_BAD_ZERO_POINT, QDG_FLAG_BAD_EXPERT_ID, QDG_FLAG_BAD_LOGIT = 1, 2, 4, 8
+QDG_L_BF16, QDG_L_F16, QDG_L_F32 = range(3)
+QDG_SCORE_SOFTMAX, QDG_SCORE_SIGMOID = range(2)
+QDG_GROUP_MAX, QDG_GROUP_TOP2 = range(2)
 
 STATUS_NAMES = {0: "QDG_OK", 1: "QDG_ERR_INVALID_ARG", 2: "QDG_ERR_UNSUPPORTED", 3: "QDG_ERR_MISALIGNED",
                 4: "QDG_ERR_WORKSPACE", 5: "QDG_ERR_HIP"}
@@ -36,7 +39,8 @@ EXPORTS = (
     "qdg_quantize_weights", "qdg_quantize_act", "qdg_plan_create", "qdg_plan_destroy", "qdg_plan_workspace",
     "qdg_plan_describe", "qdg_moe_describe", "qdg_gemm", "qdg_moe_align_capacity", "qdg_moe_align",
     "qdg_moe_gemm", "qdg_moe_combine", "qdg_moe_combine_bf16", "qdg_plan_autotune", "qdg_plan_autotune_reset",
-    "qdg_plan_jit", "qdg_gemm_noalloc",
+    "qdg_plan_jit", "qdg_gemm_noalloc", "qdg_moe_route", "qdg_quantize_act_zp", "qdg_gemm_i8_workspace",
+    "qdg_gemm_i8", "qdg_moe_gemm_i8",
 )
 
 
@@ -61,6 +65,18 @@ class TuningConfig(ctypes.Structure):
 class StdWeights(ctypes.Structure):
     _fields_ = [("qweight", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
                 ("tensor_scale", ctypes.c_void_p)]
+
+
+class RouteConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("ltype", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class I8Config(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("num_experts", ctypes.c_int32), ("otype", ctypes.c_int32),
+                ("epilogue", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class QdgError(RuntimeError):
@@ -104,6 +120,11 @@ def load():
         "qdg_plan_autotune": (I32, [P, P, P, P, P, I64, P, SZ, I32, P, P, P]),
         "qdg_plan_autotune_reset": (I32, [P]),
         "qdg_plan_jit": (I32, [P, I64, I32, ctypes.c_char_p, P]),
+        "qdg_moe_route": (I32, [P, P, I64, P, I64, P, P, P, P]),
+        "qdg_quantize_act_zp": (I32, [P, I64, I64, I64, P, I64, P, P, P]),
+        "qdg_gemm_i8_workspace": (I32, [P, I64, P]),
+        "qdg_gemm_i8": (I32, [P, P, P, P, P, P, P, P, I64, P, SZ, P]),
+        "qdg_moe_gemm_i8": (I32, [P, P, P, P, P, P, P, P, P, P, I64, I32, I32, I32, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -274,7 +295,47 @@ def qdg_plan_autotune_reset(plan):
     _check(load().qdg_plan_autotune_reset(plan.handle))
 
 
+def qdg_moe_route(cfg, logits, ld, bias, T, topk_ids, topk_weights, stream=0, status=None):
+    """status: optional device pointer to a caller-zeroed uint32 that receives QDG_FLAG_BAD_LOGIT."""
+    _check(load().qdg_moe_route(ctypes.byref(cfg), logits, ld, bias, T, topk_ids, topk_weights, status, stream))
+
+
+def qdg_quantize_act_zp(a_bf16, lda, M, k, qa, ldq, a_scales, a_zeros, stream=0):
+    _check(load().qdg_quantize_act_zp(a_bf16, lda, M, k, qa, ldq, a_scales, a_zeros, stream))
+
+
+def qdg_gemm_i8_workspace(cfg, M):
+    out = ctypes.c_size_t()
+    _check(load().qdg_gemm_i8_workspace(ctypes.byref(cfg), M, ctypes.byref(out)))
+    return out.value
+
+
+def qdg_gemm_i8(cfg, A, a_scales, a_zeros, B, b_scales, bias, Y, M, workspace=None, ws_bytes=0, stream=0):
+    _check(load().qdg_gemm_i8(ctypes.byref(cfg), A, a_scales, a_zeros, B, b_scales, bias, Y, M, workspace, ws_bytes,
+                              stream))
+
+
+def qdg_moe_gemm_i8(cfg, A, a_scales, a_zeros, B, b_scales, bias, sorted_ids, block_expert, num_padded, T, top_k,
+                    block_m, a_per_pair, Y, stream=0):
+    _check(load().qdg_moe_gemm_i8(ctypes.byref(cfg), A, a_scales, a_zeros, B, b_scales, bias, sorted_ids,
+                                  block_expert, num_padded, T, top_k, block_m, a_per_pair, Y, stream))
+
+
 # ------------------------------------------------------------- config helpers
+
+def route(num_experts, top_k, ltype=QDG_L_BF16, score=QDG_SCORE_SOFTMAX, num_groups=1, topk_groups=1,
+          group_score=QDG_GROUP_MAX, renormalize=0, scale=1.0):
+    return RouteConfig(num_experts=num_experts, top_k=top_k, ltype=ltype, score=score, num_groups=num_groups,
+                       topk_groups=topk_groups, group_score=group_score, renormalize=renormalize, scale=scale)
+
+
+def gemm_i8(n, k, lda=None, ldb=None, ldy=None, num_experts=1, otype=QDG_O_BF16, epilogue=QDG_EPI_NONE):
+    """Strides default to k rounded up to 16 bytes (A, B) and to contiguous rows (Y)."""
+    k16 = (k + 15) // 16 * 16
+    return I8Config(n=n, k=k, lda=lda or k16, ldb=ldb or k16,
+                    ldy=ldy or (n // 2 if epilogue == QDG_EPI_SILU_MUL else n), num_experts=num_experts,
+                    otype=otype, epilogue=epilogue, reserved=0)
+
 
 def layer_w4a16(n, k, asym=False, num_experts=1, otype=QDG_O_BF16):
     return LayerConfig(n=n, k=k, num_experts=num_experts, wtype=QDG_W_UINT4 if asym else QDG_W_INT4,

@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libqdg.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.cpp", "jit.cpp", "preprocess.hip", "actquant.hip", "moe_align.hip", "stream_gemm.hip", "tile_gemm.hip", "wstream_gemm.hip", "qtile_gemm.hip",
-           "wstream8_gemm.hip", "noalloc.cpp"]
+           "wstream8_gemm.hip", "noalloc.cpp", "api_ops.cpp", "moe_route.hip", "gemm_i8.hip"]
 
 COMMON = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -195,6 +195,81 @@ hipError_t launch_act_i8_planes(const int8_t* qa, int64_t rows, int64_t K, uint8
   return hipGetLastError();
 }
 
+namespace {
+
+// Asymmetric int8 per token (qdg_quantize_act_zp): one workgroup per row.
+// The range [lo, hi] of the row's finite values and 0 maps onto the 256
+// codes; scale, zero point and codes are decided in binary64 from the
+// binary32 scale.
+__global__ __launch_bounds__(256) void act_int8_zp_kernel(const uint16_t* __restrict__ a, int64_t lda, int64_t M,
+                                                          int64_t k, int8_t* __restrict__ q, int64_t ldq,
+                                                          float* __restrict__ scales, int32_t* __restrict__ zeros) {
+  __shared__ float wlo[4], whi[4];
+  for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
+    const uint16_t* x = a + row * lda;
+    float lo = 0.f, hi = 0.f;
+    for (int64_t i = threadIdx.x * 8; i < k; i += 256 * 8) {
+      // the 16 bytes start inside the row; values behind its end do not count
+      const u32x4_t v = *(const u32x4_t*)(x + i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = bf16_to_f32(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xFFFFu);
+        if (i + j < k && fabsf(f) < __builtin_inff()) {
+          lo = fminf(lo, f);
+          hi = fmaxf(hi, f);
+        }
+      }
+    }
+    for (int off = 32; off > 0; off >>= 1) {
+      lo = fminf(lo, __shfl_xor(lo, off));
+      hi = fmaxf(hi, __shfl_xor(hi, off));
+    }
+    if ((threadIdx.x & 63) == 0) {
+      wlo[threadIdx.x >> 6] = lo;
+      whi[threadIdx.x >> 6] = hi;
+    }
+    __syncthreads();
+    lo = fminf(fminf(wlo[0], wlo[1]), fminf(wlo[2], wlo[3]));
+    hi = fmaxf(fmaxf(whi[0], whi[1]), fmaxf(whi[2], whi[3]));
+    const bool any = hi > lo;
+    const float scale = any ? fmaxf((float)(((double)hi - (double)lo) / 255.0), 0x1p-126f) : 1.0f;
+    const double inv = 1.0 / (double)scale;
+    const double zero = any ? fmin(fmax(rint(-128.0 - (double)lo * inv), -128.0), 127.0) : 0.0;
+    if (threadIdx.x == 0) {
+      scales[row] = scale;
+      zeros[row] = (int32_t)zero;
+    }
+    for (int64_t i = threadIdx.x * 8; i < k; i += 256 * 8) {
+      const u32x4_t v = *(const u32x4_t*)(x + i);
+      uint32_t out[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = bf16_to_f32(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xFFFFu);
+        const double d = f == f ? rint((double)f * inv) : 0.0;
+        const int code = (int)fmin(fmax(d + zero, -128.0), 127.0);
+        out[j >> 2] |= ((uint32_t)code & 0xFFu) << (8 * (j & 3));
+      }
+      int8_t* dst = q + row * ldq + i;
+      if (i + 8 <= k) {
+        *(u32x2_t*)dst = u32x2_t{out[0], out[1]};
+      } else {
+        for (int j = 0; i + j < k; ++j) dst[j] = (int8_t)(out[j >> 2] >> (8 * (j & 3)));
+      }
+    }
+    __syncthreads();  // the row's minima are read before the next row's are written
+  }
+}
+
+}  // namespace
+
+hipError_t launch_quantize_act_zp(const void* a, int64_t lda, int64_t M, int64_t k, int8_t* qa, int64_t ldq,
+                                  float* scales, int32_t* zeros, hipStream_t s) {
+  const unsigned grid = (unsigned)(M < (1 << 20) ? M : 1 << 20);
+  hipLaunchKernelGGL(act_int8_zp_kernel, dim3(grid), dim3(256), 0, s, (const uint16_t*)a, lda, M, k, qa, ldq, scales,
+                     zeros);
+  return hipGetLastError();
+}
+
 hipError_t launch_quantize_act(int atype, const void* a, int64_t M, int64_t K, void* qa, float* scales,
                                hipStream_t s) {
   if (atype == QDG_A_INT8) {

@@ -155,6 +155,37 @@ hipError_t launch_moe_align(const int32_t* topk_ids, int64_t T, int top_k, int E
                             int64_t capacity, int32_t* sorted_ids, int32_t* block_expert,
                             int32_t* num_padded, uint32_t* status, hipStream_t s);
 
+hipError_t launch_moe_route(const qdg_route_config& c, const void* logits, int64_t ld, const float* bias, int64_t T,
+                            int32_t* topk_ids, float* topk_weights, uint32_t* status, hipStream_t s);
+hipError_t launch_quantize_act_zp(const void* a, int64_t lda, int64_t M, int64_t k, int8_t* qa, int64_t ldq,
+                                  float* scales, int32_t* zeros, hipStream_t s);
+
+// Arguments of the direct int8 product (row-major operands), dense or
+// grouped by expert.
+struct I8Args {
+  const int8_t* A;
+  const float* a_scales;
+  const int32_t* a_zeros;  // NULL: all 0
+  const int8_t* B;
+  const float* b_scales;
+  const float* bias;       // NULL: none
+  void* Y;
+  int64_t lda, ldb, ldy;
+  int M, n, k;             // M: rows of A (dense)
+  int cols;                // columns of Y (n, or n / 2 with the SiLU*mul epilogue)
+  int otype;
+  int y_vec;               // Y rows allow stores of four elements at a time
+  int32_t* partial;        // split K: int32 partials [split][M][n]
+  // grouped by expert (sorted_ids NULL: dense)
+  const int32_t* sorted_ids;
+  const int32_t* block_expert;
+  const int32_t* num_padded;
+  int num_experts, num_pairs, top_k, a_per_pair;
+};
+int gemm_i8_split(int64_t M, int64_t n, int64_t k, bool silu);
+hipError_t launch_gemm_i8(const I8Args& a, bool silu, int split, hipStream_t s);
+hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int block_m, int m_blocks, hipStream_t s);
+
 #endif
 
 }  // namespace qdg
