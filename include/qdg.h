@@ -525,9 +525,9 @@ qdg_status qdg_moe_combine_bf16(const void* y, const float* w, int64_t T, int32_
              experts are taken, never their weights); without a bias the
              experts are ordered by their logits, in which s_e increases
      groups  num_groups > 1: the E experts are num_groups equal runs; a
-             group's value is its largest c (MAX) or the sum of its two
-             largest (TOP2; without a bias c = s here); the topk_groups groups
-             with the largest values stay, equal ones the lower index first
+             group's value is the largest s + bias in it (MAX) or the sum of
+             the two largest (TOP2); the topk_groups groups with the largest
+             values stay, equal ones the lower index first
      choice  the top_k experts of the groups that stay with the largest keys,
              in descending order, equal ones the lower index first
      weight  w = s_e of the chosen, with renormalize divided by their sum

@@ -141,7 +141,7 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_rows_kernel(const I8Args p, i
   const int steps = (p.k + 63) / 64, full = p.k / 64;
   const int parts = gridDim.y * KW, part = blockIdx.y * KW + wave;
   const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
-#pragma unroll 4
+#pragma unroll 1
   for (int s = s0; s < min(s1, full); ++s) {
     u32x4_t a[MT], b[NT];
 #pragma unroll
