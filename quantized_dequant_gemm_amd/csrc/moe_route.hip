@@ -4,26 +4,33 @@
 //   value of a group = largest c or sum of its two largest; the best groups
 //   stay; top_k of what stays by c; w = s, renormalised, scaled.
 //
-// One wave per token, EPL consecutive experts per lane (one vector load).
-// Each round takes the wave-wide largest key with six DPP maxima and finds
-// its owner with ballots.
+// One wave per token, EPL consecutive experts per lane (one vector load). A
+// key becomes one unsigned number: its binary32 bits in increasing order,
+// the lowest bits replaced by the expert's index counted from the top, so
+// that a round of the top_k is one wave-wide unsigned maximum (six DPP
+// steps): it names the expert, and equal keys give the lowest index.
 //
-// A choice must not hang on binary32 rounding, yet binary64 scores for every
-// expert and 64-bit reductions cost three times the whole of the rest
-// (8192 x 256 grouped: 31 us). So a key is an interval [lo, up] around
-// its binary32 value that holds the exact one: the largest lower bound m of a
-// round leaves the experts with up >= m as candidates, nearly always one. Where
-// there are more, and where the intervals of group values overlap at the border
-// of what stays, the wave computes those keys in binary64. Without a bias the
-// keys are the logits themselves, exact (lo = up).
+// A choice must not hang on binary32 rounding, yet binary64 scores and 64-bit
+// reductions for all experts take twice the time (8192 tokens x 256 experts
+// in groups: 31 us). So the top_k + 1 largest are taken in binary32 and the
+// gaps between neighbours are compared with what the keys can be off by. Where
+// a gap does not decide (some 4 % of the tokens of normal logits and biases), eight
+// more candidates are taken and ranked by binary64 keys, one lane each; if
+// not even these hold the top_k for sure, the whole token is routed in binary64.
+// Without a bias the keys are the logits: exact for 16-bit types, cut by the
+// index bits for binary32 ones.
 //
-// Bounds of the binary32 scores (with a factor of two or more to spare):
-// exp by v_exp_f32 of x * log2(e) is off by at most 2^-23 + 1.5 |x| 2^-24
-// relative; 1 / (1 + t) adds 2^-24 + 2^-23 and does not widen what t brings:
-// sigmoid 2^-20 + |x| 2^-22. Softmax subtracts first (|d| 2^-24 more) and
-// divides by a sum whose terms with mass have |d| below about ln(1024):
-// 2^-19 + |d| 2^-22. Adding the bias rounds by 2^-24 of the key: 2^-23.
-// The weights of the top_k are computed in binary64, one lane each.
+// Error bounds (with a factor of two or more to spare): exp as v_exp_f32 of
+// x * log2(e) is off by 2^-23 + 1.5 |x| 2^-24 relative. Sigmoid: 1 / (1 + t)
+// adds 2^-24 + 2^-23 and passes on s (1 - s) of t's error, and s (1 - s) |x|
+// < 0.3: off by less than 2^-21 absolute. Softmax subtracts first (|d| 2^-24
+// more, s |d| < 0.4) and divides by a sum whose terms with mass have |d|
+// below about ln(1024): less than 2^-20. kScoreErr = 2^-19 for both, and the
+// bias added rounds by 2^-24 of the key.
+//
+// The weights of the top_k, one lane each: exp in binary32 (one unit in the
+// last place, 2^-23) of the argument's upper part, times 1 + its lower part;
+// sums and quotients in binary64, so a weight is off by 2^-22 + 2^-24.
 #include <algorithm>
 
 #include "qdg_device.h"
@@ -34,23 +41,36 @@ namespace {
 
 constexpr double kNegInf64 = -__builtin_inf();
 constexpr float kInf = __builtin_inff();
+constexpr float kMax = 3.402823466e+38f;  // largest finite
 constexpr int kWavesPerBlock = 4;
+constexpr float kScoreErr = 0x1p-19f;
+constexpr int kMore = 8;  // candidates beyond top_k where the order is in doubt
 
+// One step of a maximum over the wave: lanes without a source, and rows
+// outside ROW_MASK, see 0.
 template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ float dpp_f32(float v) {
-  const int i = __builtin_bit_cast(int, v);
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, ROW_MASK, 0xF, false));
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, false));
 }
 
-// Largest value of the wave (NaN ignored), in every lane.
-__device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, dpp_f32<0x111, 0xF>(v));  // row_shr:1, 2, 4, 8: lane 15 of each row of 16
-  v = fmaxf(v, dpp_f32<0x112, 0xF>(v));
-  v = fmaxf(v, dpp_f32<0x114, 0xF>(v));
-  v = fmaxf(v, dpp_f32<0x118, 0xF>(v));
-  v = fmaxf(v, dpp_f32<0x142, 0xA>(v));  // row_bcast:15 into rows 1 and 3
-  v = fmaxf(v, dpp_f32<0x143, 0xC>(v));  // row_bcast:31 into rows 2 and 3
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+// Largest value of the wave, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = dpp_max<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8: lane 15 of each row of 16
+  v = dpp_max<0x112, 0xF>(v);
+  v = dpp_max<0x114, 0xF>(v);
+  v = dpp_max<0x118, 0xF>(v);
+  v = dpp_max<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  v = dpp_max<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Binary32 <-> unsigned in the same order.
+__device__ __forceinline__ uint32_t order_of(float f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_order(uint32_t o) {
+  return __builtin_bit_cast(float, o ^ (~(uint32_t)((int32_t)o >> 31) | 0x80000000u));
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -60,6 +80,23 @@ __device__ __forceinline__ double wave_sum(double v) {
 
 __device__ __forceinline__ float readlane_f32(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+__device__ __forceinline__ double readlane_f64(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ void top2_add(float& m1, float& m2, float v) {
+  m2 = __builtin_amdgcn_fmed3f(m1, m2, v);
+  m1 = fmaxf(m1, v);
+}
+
+__device__ __forceinline__ void sort2(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
 }
 
 __device__ __forceinline__ float logit_f32(uint16_t h, int ltype) {
@@ -118,13 +155,6 @@ __device__ __forceinline__ void load_row(const void* row, int ltype, bool vec, i
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
-// The two largest of a pair of ordered pairs.
-__device__ __forceinline__ void top2_merge(float& m1, float& m2, float o1, float o2) {
-  const float lo = fminf(m1, o1);
-  m1 = fmaxf(m1, o1);
-  m2 = fmaxf(lo, fmaxf(m2, o2));
-}
-
 // What the rare binary64 decisions read again: one token's row (cached by
 // then), so that they keep no registers of the common path alive.
 struct Row {
@@ -136,7 +166,7 @@ struct Row {
 
   __device__ __forceinline__ float logit(int e) const {
     const float x = ltype == QDG_L_F32 ? ((const float*)logits)[e] : logit_f32(((const uint16_t*)logits)[e], ltype);
-    return x != x ? -kInf : fminf(x, 3.402823466e+38f);
+    return x != x ? -kInf : fminf(x, kMax);
   }
   __device__ __forceinline__ double key64(int e) const {
     const float x = logit(e), b = bias ? bias[e] : 0.f;
@@ -186,42 +216,95 @@ __device__ __forceinline__ uint64_t groups64(Row& row, const qdg_route_config& c
   return __ballot(lane < G && rank < c.topk_groups);
 }
 
-// The expert with the largest binary64 key among the candidates (bit j of
-// cand: the lane's expert e0 + j), equal ones the lowest.
-__device__ __forceinline__ int best64(Row& row, uint32_t cand, int e0, int lane) {
-  if (row.score == QDG_SCORE_SOFTMAX) row.set_sum(lane);
-  double best = kNegInf64;
-  int at = 1 << 30;
-  for (; cand; cand &= cand - 1) {
-    const int e = e0 + __builtin_ctz(cand);
-    const double k = row.key64(e);
-    if (at == 1 << 30 || k > best) {
-      best = k;
-      at = e;
-    }
-  }
+// A token routed in binary64: the id that lane r < top_k takes.
+__device__ __forceinline__ int route64(Row& row, const qdg_route_config& c, uint64_t stay, int lane) {
+  const int E = c.num_experts, per = E / c.num_groups;
+  if (row.score == QDG_SCORE_SOFTMAX && row.bias) row.set_sum(lane);
+  uint32_t taken = 0;  // bit i: expert lane + 64 i
+  int id = 0;
 #pragma unroll 1
-  for (int d = 32; d > 0; d >>= 1) {
-    const double ob = __shfl_xor(best, d);
-    const int oa = __shfl_xor(at, d);
-    if (oa != 1 << 30 && (at == 1 << 30 || ob > best || (ob == best && oa < at))) {
-      best = ob;
-      at = oa;
+  for (int r = 0; r < c.top_k; ++r) {
+    double best = kNegInf64;
+    int at = 1 << 30;
+#pragma unroll 1
+    for (int e = lane, i = 0; e < E; e += 64, ++i) {
+      if ((taken >> i & 1) || !(stay >> (e / per) & 1)) continue;
+      const double k = row.bias ? row.key64(e) : (double)row.logit(e);
+      if (at == 1 << 30 || k > best) {
+        best = k;
+        at = e;
+      }
     }
+#pragma unroll 1
+    for (int d = 32; d > 0; d >>= 1) {
+      const double ob = __shfl_xor(best, d);
+      const int oa = __shfl_xor(at, d);
+      if (oa != 1 << 30 && (at == 1 << 30 || ob > best || (ob == best && oa < at))) {
+        best = ob;
+        at = oa;
+      }
+    }
+    if ((at & 63) == lane) taken |= 1u << (at >> 6);
+    if (r == lane) id = at;
   }
-  return __builtin_amdgcn_readfirstlane(at);
+  return id;
+}
+
+// The largest of the wave's ordered keys, taken out (0: none is left). Up to
+// four per lane are sorted, so that the first is the lane's largest.
+template <int EPL>
+__device__ __forceinline__ uint32_t take_largest(uint32_t (&o)[EPL]) {
+  uint32_t m = o[0];
+  if constexpr (EPL > 4) {
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) m = max(m, o[j]);
+  }
+  m = wave_max(m);
+  if constexpr (EPL > 4) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) o[j] = o[j] == m ? 0u : o[j];
+  } else {
+    const bool pop = o[0] == m;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) o[j] = pop ? (j + 1 < EPL ? o[j + 1] : 0u) : o[j];
+  }
+  return m;
+}
+
+// Bounds of the exact key behind an ordered one whose low bits are cut.
+__device__ __forceinline__ float key_low(uint32_t o, uint32_t index_mask) {
+  const float k = of_order(o & ~index_mask);
+  return k - kScoreErr - fabsf(k) * 0x1p-23f;
+}
+__device__ __forceinline__ float key_high(uint32_t o, uint32_t index_mask) {
+  const float k = of_order(o | index_mask);
+  return k + kScoreErr + fabsf(k) * 0x1p-23f;
+}
+
+// exp(a - b) for a <= b in binary64 with binary32's relative error 2^-23,
+// 0 below 2^-126.
+__device__ __forceinline__ double exp_diff(float a, float b) {
+  const double d = (double)a - (double)b;
+  const float hi = (float)d, lo = (float)(d - (double)hi);
+  const float e = expf(hi);
+  return (double)__builtin_fmaf(e, lo, e);
+}
+
+// 1 / v, off by less than 2^-40.
+__device__ __forceinline__ double rcp64(double v) {
+  const double r = __builtin_amdgcn_rcp(v);
+  return __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
 }
 
 template <int EPL>
 __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
     const qdg_route_config c, const void* __restrict__ logits, int64_t ld, const float* __restrict__ bias, int64_t T,
-    bool vec, int group_shift, int32_t* __restrict__ ids, float* __restrict__ weights,
+    bool vec, int group_shift, uint32_t index_mask, int32_t* __restrict__ ids, float* __restrict__ weights,
     uint32_t* __restrict__ status) {
-  __shared__ float2 keybuf[kWavesPerBlock][EPL * 64];
+  __shared__ float keybuf[kWavesPerBlock][EPL * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int E = c.num_experts, G = c.num_groups, per = E / G, e0 = lane * EPL;
-  const float nan = __builtin_nanf("");
   float b[EPL];
   bool bad_bias = false;
 #pragma unroll
@@ -234,169 +317,175 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
     float x[EPL];  // logits, -inf where masked by the logit
     load_row<EPL>(row.logits, c.ltype, vec, e0, E, -kInf, x);
     bool bad = bad_bias;
-    float top = -kInf;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       bad |= x[j] != x[j] || x[j] == kInf;
-      x[j] = x[j] != x[j] ? -kInf : fminf(x[j], 3.402823466e+38f);
-      top = fmaxf(top, x[j]);
+      x[j] = x[j] != x[j] ? -kInf : fminf(x[j], kMax);
     }
     if (status && bad) atomicOr(status, (uint32_t)QDG_FLAG_BAD_LOGIT);
+    if (c.score == QDG_SCORE_SOFTMAX) {
+      float top = x[0];
+#pragma unroll
+      for (int j = 1; j < EPL; ++j) top = fmaxf(top, x[j]);
+      row.top = of_order(wave_max(order_of(top)));
+    }
 
-    // intervals of the keys; without a bias of the scores, for the groups
-    const bool score_keys = bias || G > 1;
-    float lo[EPL], up[EPL];
-    if (c.score == QDG_SCORE_SOFTMAX) row.top = top = wave_max(top);
-    if (score_keys) {
+    float key[EPL];  // s + bias; -inf where masked
+    if (bias || G > 1) {
       float inv = 1.f;
       if (c.score == QDG_SCORE_SOFTMAX) {
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-          lo[j] = x[j] == -kInf ? 0.f : __expf(x[j] - top);
-          sum += lo[j];
+          key[j] = x[j] == -kInf ? 0.f : __expf(x[j] - row.top);
+          sum += key[j];
         }
         for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
-        inv = sum > 0.f ? 1.0f / sum : 0.f;
+        inv = __builtin_amdgcn_rcpf(sum);
       }
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        float s, ds;
-        if (c.score == QDG_SCORE_SOFTMAX) {
-          s = lo[j] * inv;
-          ds = s * (0x1p-19f + (top - x[j]) * 0x1p-22f);
-        } else {
-          s = __builtin_amdgcn_rcpf(1.0f + __expf(-x[j]));
-          ds = s * (0x1p-20f + fabsf(x[j]) * 0x1p-22f);
-        }
-        // a score below 2^-126 (flushed, or with a lost mantissa) is off by less than that
-        ds += 0x1p-125f;
-        if (!(ds < kInf)) ds = 0x1p-125f;  // |x| so large that s is 0 or 1 to the last bit
-        const float k = s + b[j];
-        const float d = ds + fabsf(k) * 0x1p-23f;
-        const bool masked = x[j] == -kInf || !(b[j] > -kInf), fin = fabsf(k) < kInf;
-        lo[j] = masked ? -kInf : fin ? fmaxf(k - d, -3.402823466e+38f) : k;
-        up[j] = masked ? -kInf : fin ? k + d : k;
+        const float s = c.score == QDG_SCORE_SOFTMAX ? key[j] * inv : __builtin_amdgcn_rcpf(1.0f + __expf(-x[j]));
+        key[j] = x[j] == -kInf || !(b[j] > -kInf) ? -kInf : s + b[j];
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) lo[j] = up[j] = x[j];
     }
 
     uint64_t stay = ~0ull;
     if (G > 1) {
-      // lane g of the result: the interval of group g's value
-      float l1 = -kInf, l2 = -kInf, u1 = -kInf, u2 = -kInf;
-      int owner = lane;  // the lane that holds group g = lane's interval
+      float m1 = -kInf, m2 = -kInf;  // lane of group g: its two largest keys
+      int owner = lane;              // the lane that holds group g = lane's
       if (group_shift >= 0) {
         // a group is 2^group_shift whole lanes
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          top2_merge(l1, l2, e0 + j < E ? lo[j] : -kInf, -kInf);
-          top2_merge(u1, u2, e0 + j < E ? up[j] : -kInf, -kInf);
-        }
+        for (int j = 0; j < EPL; ++j) top2_add(m1, m2, e0 + j < E ? key[j] : -kInf);
         for (int m = 1; m < 1 << group_shift; m <<= 1) {
-          top2_merge(l1, l2, __shfl_xor(l1, m), __shfl_xor(l2, m));
-          top2_merge(u1, u2, __shfl_xor(u1, m), __shfl_xor(u2, m));
+          const float o1 = __shfl_xor(m1, m), o2 = __shfl_xor(m2, m);
+          m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+          m1 = fmaxf(m1, o1);
         }
         owner = lane << group_shift;
       } else {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) keybuf[wave][e0 + j] = make_float2(lo[j], up[j]);
+        for (int j = 0; j < EPL; ++j) keybuf[wave][e0 + j] = key[j];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         if (lane < G)
-          for (int i = 0; i < per; ++i) {
-            const float2 k = keybuf[wave][lane * per + i];
-            top2_merge(l1, l2, k.x, -kInf);
-            top2_merge(u1, u2, k.y, -kInf);
-          }
+          for (int i = 0; i < per; ++i) top2_add(m1, m2, keybuf[wave][lane * per + i]);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
       }
-      const bool one = c.group_score == QDG_GROUP_MAX;
-      float vl = one || l2 == -kInf ? l1 : l1 + l2, vu = one || u2 == -kInf ? u1 : u1 + u2;
-      if (!one) {  // the two sums' own rounding
-        if (fabsf(vl) < kInf) vl -= fabsf(vl) * 0x1p-23f;
-        if (fabsf(vu) < kInf) vu += fabsf(vu) * 0x1p-23f;
-      }
-      vl = __shfl(vl, owner & 63);
-      vu = __shfl(vu, owner & 63);
-      int maybe = 0, sure = 0;  // groups that may be ahead of this lane's, and that are
+      float v = c.group_score == QDG_GROUP_MAX || m2 == -kInf ? m1 : m1 + m2;
+      // two keys' errors and the roundings of keys and sum
+      const float err = fabsf(v) < kInf ? 2.f * kScoreErr + (fabsf(m1) + (m2 == -kInf ? 0.f : fabsf(m2))) * 0x1p-22f : 0.f;
+      v = __shfl(v, owner & 63);
+      const float dv = __shfl(err, owner & 63);
+      const float vl = v - dv, vu = v + dv;
+      int maybe = 0;  // groups that may be ahead of this lane's
       for (int g = 0; g < G; ++g) {
-        const float ol = readlane_f32(vl, g), ou = readlane_f32(vu, g);
+        const float ou = readlane_f32(vu, g);
         const bool tie = ou == -kInf && vu == -kInf;  // all masked, both: the index decides
         maybe += g != lane && (tie ? g < lane : ou >= vl);
-        sure += g != lane && (tie ? g < lane : ol > vu);
       }
-      const bool in = lane < G && maybe < c.topk_groups, out = sure >= c.topk_groups;
+      const bool in = lane < G && maybe < c.topk_groups;
       stay = __ballot(in);
-      if (__ballot(lane < G && !in && !out)) stay = groups64(row, c, lane);
+      if (__popcll(stay) != c.topk_groups) stay = groups64(row, c, lane);
     }
-    const bool exact = !bias;  // the keys are the logits
+
+    // the ordered keys
     const bool lane_stays = group_shift < 0 || (stay >> (lane >> group_shift)) & 1;
+    uint32_t o[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      if (exact) lo[j] = up[j] = x[j];
       const int e = e0 + j;
       const bool stays = group_shift < 0 && G > 1 ? e < E && (stay >> (e / per)) & 1 : lane_stays;
-      if (e >= E || !stays) lo[j] = up[j] = nan;  // not to be taken
+      // -0 and 0 are one key
+      o[j] = e < E && stays ? (order_of((bias ? key[j] : x[j]) + 0.f) & ~index_mask) | (index_mask - (uint32_t)e) : 0u;
     }
-
-    int my_id = 0;
-    float my_x = -kInf;  // -inf: masked, weight 0
-    for (int r = 0; r < c.top_k; ++r) {
-      float m = lo[0];
-#pragma unroll
-      for (int j = 1; j < EPL; ++j) m = fmaxf(m, lo[j]);
-      m = wave_max(m);
-      uint32_t cand = 0;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) cand |= (uint32_t)(up[j] >= m) << j;
-      const uint64_t has = __ballot(cand != 0), more = __ballot((cand & (cand - 1)) != 0);
-      int wl, ws;
-      if (exact || m == -kInf || ((has & (has - 1)) == 0 && more == 0)) {
-        wl = __builtin_ctzll(has);
-        ws = __builtin_ctz(__builtin_amdgcn_readlane(cand, wl));
-      } else {
-        const int e = best64(row, cand, e0, lane);
-        wl = e / EPL;
-        ws = e % EPL;
-      }
-      float won = 0.f;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j)
-        if (j == ws) {
-          won = x[j];
-          if (lane == wl) lo[j] = up[j] = nan;
+    if constexpr (EPL == 2) sort2(o[0], o[1]);
+    if constexpr (EPL == 4) {
+      sort2(o[0], o[1]);
+      sort2(o[2], o[3]);
+      sort2(o[0], o[2]);
+      sort2(o[1], o[3]);
+      sort2(o[1], o[2]);
+    }
+    // rounds 0 .. top_k: lane r keeps the r-th largest
+    uint32_t mine = 0;
+    for (int r = 0; r <= c.top_k; ++r) {
+      const uint32_t m = take_largest<EPL>(o);
+      mine = lane == r ? m : mine;
+    }
+    if (bias || c.ltype == QDG_L_F32) {
+      // does each gap to the next decide?
+      const uint32_t next = (uint32_t)__shfl_down((int)mine, 1);
+      const bool checked = lane < c.top_k && next != 0 && (mine & ~index_mask) != (order_of(-kInf) & ~index_mask);
+      const bool sure = bias ? key_low(mine, index_mask) > key_high(next, index_mask)
+                             : (mine ^ next) > index_mask;  // exact but for the cut bits
+      if (__ballot(checked && !sure)) {
+        // kMore candidates more, ranked by binary64 keys, one lane each
+        uint32_t last = 0;
+        for (int r = c.top_k + 1; r < c.top_k + kMore; ++r) {
+          last = take_largest<EPL>(o);
+          mine = lane == r ? last : mine;
         }
-      won = readlane_f32(won, wl);
-      if (lane == r) {
-        my_id = wl * EPL + ws;
-        my_x = m == -kInf ? -kInf : won;  // only masked experts are left
+        if (c.score == QDG_SCORE_SOFTMAX && bias) row.set_sum(lane);
+        int cand = (int)(index_mask - (mine & index_mask));
+        double k = kNegInf64;
+        if (mine != 0) k = bias ? row.key64(cand) : (double)row.logit(cand);
+        else cand = 1 << 30;
+        int rank = 0;
+        for (int i = 0; i < c.top_k + kMore; ++i) {
+          const double ok = readlane_f64(k, i);
+          const int oc = __builtin_amdgcn_readlane(cand, i);
+          rank += ok > k || (ok == k && oc < cand);
+        }
+        // what was not taken is at most `last`; masked experts follow the index
+        const uint64_t kth = __ballot(lane < c.top_k + kMore && rank == c.top_k - 1);
+        const double kth_key = readlane_f64(k, __builtin_ctzll(kth));
+        const double rest = bias ? (double)key_high(last, index_mask) : (double)of_order(last | index_mask);
+        const bool whole = last == 0 || (last & ~index_mask) == (order_of(-kInf) & ~index_mask);
+        int id = 0;
+        if (whole || kth_key > rest) {
+          for (int i = 0; i < c.top_k + kMore; ++i) {
+            const int to = __builtin_amdgcn_readlane(rank, i), oc = __builtin_amdgcn_readlane(cand, i);
+            if (lane == to) id = oc;
+          }
+        } else {
+          id = route64(row, c, stay, lane);
+        }
+        mine = index_mask - (uint32_t)id;
       }
     }
+    const int id = (int)(index_mask - (mine & index_mask));
 
-    // the weights, one lane each
-    double w = 0.0;
-    if (c.score == QDG_SCORE_SIGMOID) {
-      if (my_x != -kInf) w = sigmoid64((double)my_x);
-      if (c.renormalize) {
-        const double sum = wave_sum(w);
-        w = sum > 0.0 ? w / sum : 0.0;
-      }
-    } else {
-      // renormalised weights need no more than the chosen experts' ratios
-      const float ref = c.renormalize ? wave_max(my_x) : top;
-      if (my_x != -kInf) w = exp((double)my_x - (double)ref);
-      if (c.renormalize)
-        row.sum64 = wave_sum(w);
-      else
-        row.set_sum(lane);
-      w = row.sum64 > 0.0 ? w / row.sum64 : 0.0;
-    }
+    // the weights
+    float my_x = -kInf;
     if (lane < c.top_k) {
-      ids[t * c.top_k + lane] = my_id;
+      my_x = row.logit(id);
+      if (bias && !(bias[id] > -kInf)) my_x = -kInf;  // masked: weight 0
+    }
+    double w = 0.0;
+    const bool sigmoid = c.score == QDG_SCORE_SIGMOID;
+    // renormalised softmax weights need no more than the chosen experts' ratios
+    const float ref = sigmoid ? 0.f : c.renormalize ? of_order(wave_max(order_of(my_x))) : row.top;
+    const float arg = sigmoid ? my_x : my_x - ref;
+    if (__ballot(my_x != -kInf && arg < -80.f)) {  // near or past the end of binary32
+      if (my_x != -kInf) w = sigmoid ? sigmoid64((double)my_x) : exp((double)my_x - (double)ref);
+    } else if (my_x != -kInf) {
+      w = sigmoid ? rcp64(1.0 + (double)expf(-my_x)) : exp_diff(my_x, ref);
+    }
+    if (c.renormalize) {
+      row.sum64 = w;
+      for (int m = 1; m < c.top_k; m <<= 1) row.sum64 += __shfl_xor(row.sum64, m);
+    } else if (!sigmoid) {
+      double sum = 0.0;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) sum += x[j] == -kInf ? 0.0 : exp_diff(x[j], row.top);
+      row.sum64 = wave_sum(sum);
+    }
+    if (c.renormalize || !sigmoid) w = row.sum64 > 0.0 ? w * rcp64(row.sum64) : 0.0;
+    if (lane < c.top_k) {
+      ids[t * c.top_k + lane] = id;
       weights[t * c.top_k + lane] = (float)(w * (double)c.scale);
     }
   }
@@ -415,9 +504,11 @@ hipError_t launch_moe_route(const qdg_route_config& c, const void* logits, int64
   const int lanes = per / epl;  // whole lanes of a group, where it is that
   const int group_shift =
       c.num_groups > 1 && per % epl == 0 && (lanes & (lanes - 1)) == 0 ? __builtin_ctz(lanes) : -1;
+  uint32_t index_mask = 0;
+  while ((int)index_mask + 1 < c.num_experts) index_mask = index_mask * 2 + 1;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(64 * kWavesPerBlock), 0, s, c, logits, ld, bias, T, vec, group_shift, ids,
-                       weights, status);
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * kWavesPerBlock), 0, s, c, logits, ld, bias, T, vec, group_shift,
+                       index_mask, ids, weights, status);
     return hipGetLastError();
   };
   switch (epl) {
