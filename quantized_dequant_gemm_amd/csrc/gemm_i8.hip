@@ -257,6 +257,253 @@ hipError_t launch_rows(const I8Args& a, bool silu, int m_blocks, int split, hipS
                    : go(gemm_i8_rows_kernel<MT, NT, KW, false, false, MOE>);
 }
 
+// ------------------------------------------------------------- LDS tiles
+// Many rows: a BM x BN tile of Y per workgroup, 32 x 32 MFMA tiles, K in
+// groups of 128 bytes through NS stages of LDS. A stage holds the rows of A
+// and B as they are stored (128 bytes a row), copied by direct global -> LDS
+// loads of 16 bytes a lane; the chunk of 16 bytes at slot j of row r is chunk
+// j ^ f(r), so that the 16-byte fragment reads of 8 (or 16) neighbouring rows fall on
+// different banks without padding.
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((ext_vector_type(16))) int i32x16_t;
+
+__device__ __forceinline__ i32x16_t mfma_i8_32(u32x4_t a, u32x4_t b, i32x16_t c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0,
+                                               0);
+}
+
+__device__ __forceinline__ int i8_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+// The copies of group g into one stage: every wave issues the same number.
+// Chunks behind the row's end read the row's last chunk instead (masked
+// before use).
+template <int BM, int BN, int NW, int TAG>
+__device__ __forceinline__ void i8_load_stage(char* st, const int8_t* const (&src)[(BM + BN) / 8 / NW], int wave,
+                                              int lane, int g, int last_chunk) {
+#pragma unroll
+  for (int q = 0; q < (BM + BN) / 8 / NW; ++q) {
+    const int i = q * NW + wave;  // rows 8 i .. 8 i + 7 of the stage
+    const int ch = (lane & 7) ^ (lane >> 3) ^ (i & 1);
+    const uint32_t off = (uint32_t)min(g * 8 + ch, last_chunk) * 16u;
+    __builtin_amdgcn_global_load_lds(src[q] + off, (lds_void*)(st + i * 1024), 16, 0, 0);
+  }
+}
+
+// Zeroes the bytes from k on of the 16 at byte kk of a row.
+__device__ __forceinline__ u32x4_t i8_mask(u32x4_t v, int kk, int k) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const int b = k - kk - 4 * d;
+    v[d] &= b >= 4 ? ~0u : b <= 0 ? 0u : (1u << (8 * b)) - 1;
+  }
+  return v;
+}
+
+// One group of a wave's (32 TM) x (32 TN) tile.
+template <int TM, int TN, bool ZP, bool MASK, int TAG>
+__device__ __forceinline__ void i8_group(const char* st, int a_lane, int b_lane, int sw, int half, int kk, int k,
+                                         i32x16_t (&acc)[TM][TN], int (&zs)[TN]) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int at = ((2 * s + half) ^ sw) * 16;
+    u32x4_t a[TM], b[TN];
+#pragma unroll
+    for (int t = 0; t < TN; ++t) b[t] = *(const u32x4_t*)(st + b_lane + t * 4096 + at);
+#pragma unroll
+    for (int t = 0; t < TM; ++t) a[t] = *(const u32x4_t*)(st + a_lane + t * 4096 + at);
+    if constexpr (MASK) {
+      const int at_k = kk + (2 * s + half) * 16;
+#pragma unroll
+      for (int t = 0; t < TN; ++t) b[t] = i8_mask(b[t], at_k, k);
+#pragma unroll
+      for (int t = 0; t < TM; ++t) a[t] = i8_mask(a[t], at_k, k);
+    }
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      if constexpr (ZP) zs[t] = i8_sum16(b[t], zs[t]);
+#pragma unroll
+      for (int m = 0; m < TM; ++m) acc[m][t] = mfma_i8_32(b[t], a[m], acc[m][t]);
+    }
+  }
+}
+
+template <int WM, int WN, int TM, int TN, int NS, bool SILU, bool ZP, bool MOE>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args p, int m_blocks, int n_blocks) {
+  constexpr int NW = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN, BYTES = (BM + BN) * 128;
+  constexpr int LOADS = (BM + BN) / 8 / NW, TAG = ((WM * 8 + WN) * 8 + TM) * 64 + TN * 8 + SILU * 4 + ZP * 2 + MOE;
+  static_assert((BM + BN) / 8 % NW == 0, "every wave issues the same number of copies");
+  static_assert(NS == 2 || NS == 3, "two or three stages");
+  static_assert(NS * BYTES <= 160 * 1024, "stages exceed LDS");
+  __shared__ __attribute__((aligned(1024))) char st0[BYTES];
+  __shared__ __attribute__((aligned(1024))) char st1[BYTES];
+  __shared__ __attribute__((aligned(1024))) char st2[NS == 3 ? BYTES : 16];
+  char* const stage[3] = {st0, st1, st2};
+  const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  int mb, nb;
+  if constexpr (MOE) {
+    moe_tile_order(n_blocks, mb, nb);
+    if (mb >= m_blocks) return;  // the grid covers whole groups of 8 blocks
+  } else {
+    // XCD x takes the x-th eighth of the tile order, which walks 4 x 8 blocks
+    // of tiles (as in the 8-bit tiles over packed weights)
+    const int total = m_blocks * n_blocks;
+    int lin = blockIdx.x;
+    if (total % 8 == 0) lin = (lin % 8) * (total / 8) + lin / 8;
+    if (m_blocks % 4 == 0 && n_blocks % 8 == 0) {
+      const int sb = lin / 32, w = lin % 32;
+      mb = (sb / (n_blocks / 8)) * 4 + w / 8;
+      nb = (sb % (n_blocks / 8)) * 8 + w % 8;
+    } else {
+      mb = lin / n_blocks;
+      nb = lin % n_blocks;
+    }
+  }
+  int expert = 0;
+  if constexpr (MOE) {
+    if (mb * BM >= *p.num_padded) return;
+    expert = p.block_expert[mb];
+    if ((unsigned)expert >= (unsigned)p.num_experts) return;
+  }
+  // 16-column tiles of B in the order the epilogue wants (gate and up tiles
+  // alternate with SILU)
+  const int vt0 = nb * (BN / 16);
+  const int8_t* src[LOADS];
+#pragma unroll
+  for (int q = 0; q < LOADS; ++q) {
+    const int row = (q * NW + wave) * 8 + (lane >> 3);  // stage row: A, then B
+    if (row < BM) {
+      const int grow = mb * BM + row;
+      int ar = min(grow, p.M - 1);
+      if constexpr (MOE) {
+        const int id = p.sorted_ids[grow];
+        ar = (unsigned)id < (unsigned)p.num_pairs ? (p.a_per_pair ? id : id / p.top_k) : 0;
+      }
+      src[q] = p.A + (int64_t)ar * p.lda;
+    } else {
+      int first, rows;
+      i8_tile<SILU>(p, vt0 + (row - BM) / 16, first, rows);
+      // tiles behind the layer read row 0; their results are never stored
+      const int br = rows > 0 ? first + min((row - BM) % 16, rows - 1) : 0;
+      src[q] = p.B + ((int64_t)expert * p.n + br) * p.ldb;
+    }
+  }
+  const int groups = (p.k + 127) / 128, last_chunk = (p.k - 1) / 16;
+  const int a_lane = (wm * TM * 32 + r) * 128, b_lane = (BM + wn * TN * 32 + r) * 128, sw = i8_swizzle(r);
+  i32x16_t acc[TM][TN];
+  int zs[TN];
+#pragma unroll
+  for (int t = 0; t < TN; ++t) {
+    zs[t] = 0;
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[m][t][i] = 0;
+  }
+#pragma unroll
+  for (int q = 0; q < NS - 1; ++q)
+    i8_load_stage<BM, BN, NW, TAG>(stage[q], src, wave, lane, min(q, groups - 1), last_chunk);
+  const int full = p.k / 128;  // groups that need no mask
+  int g = 0;
+  for (; g + NS <= full; g += NS) {
+#pragma unroll
+    for (int cur = 0; cur < NS; ++cur) {
+      // this wave's copies of group g + cur have landed; those of the NS - 2
+      // groups behind it stay in flight
+      constexpr int LEFT = LOADS * (NS - 2);
+      __builtin_amdgcn_s_waitcnt((LEFT & 15) | (7 << 4) | (15 << 8) | ((LEFT >> 4) << 14));
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      asm volatile("s_barrier" ::: "memory");
+      i8_load_stage<BM, BN, NW, TAG + 65536>(stage[(cur + NS - 1) % NS], src, wave, lane,
+                                             min(g + cur + NS - 1, groups - 1), last_chunk);
+      i8_group<TM, TN, ZP, false, TAG>(stage[cur], a_lane, b_lane, sw, half, 0, 0, acc, zs);
+    }
+  }
+  // the remaining groups, the last one cut at k: copies for the first NS - 1
+  // of them are in flight
+#pragma unroll 1
+  for (; g < groups; g += NS) {
+#pragma unroll
+    for (int cur = 0; cur < NS; ++cur) {
+      if (g + cur < groups) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        i8_load_stage<BM, BN, NW, TAG + 131072>(stage[(cur + NS - 1) % NS], src, wave, lane,
+                                                min(g + cur + NS - 1, groups - 1), last_chunk);
+        i8_group<TM, TN, ZP, true, TAG>(stage[cur], a_lane, b_lane, sw, half, (g + cur) * 128, p.k, acc, zs);
+      }
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);  // the trailing copies have landed
+  __syncthreads();
+
+  // column sums of B into the order of the result's rows
+  int* zbuf = (int*)st0 + wave * TN * 32;
+  if constexpr (ZP) {
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      const int z = zs[t] + __shfl_xor(zs[t], 32);
+      if (half == 0) zbuf[t * 32 + r] = z;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // a lane holds row r of each 32-row tile and, of each 32-column tile, the
+  // columns 8 q + 4 half .. + 3
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    const int grow = mb * BM + (wm * TM + m) * 32 + r;
+    int yr = grow, ar = grow;
+    bool real = grow < p.M;
+    if constexpr (MOE) {
+      yr = p.sorted_ids[grow];
+      real = (unsigned)yr < (unsigned)p.num_pairs;
+      ar = p.a_per_pair ? yr : yr / p.top_k;
+    }
+    if (!real) continue;
+    const int za = ZP ? p.a_zeros[ar] : 0;
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      i32x4_t v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        i32x4_t z = {0, 0, 0, 0};
+        if constexpr (ZP) z = *(const i32x4_t*)(zbuf + t * 32 + q * 8 + half * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[q][i] = acc[m][t][q * 4 + i] - za * z[i];
+      }
+      const int vt = vt0 + (wn * TN + t) * 2;  // two 16-column tiles of B
+      if constexpr (SILU) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) i8_finish<SILU>(p, v[q], v[q + 2], yr, ar, expert, vt * 8 + q * 8 + half * 4);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) i8_finish<SILU>(p, v[q], v[q], yr, ar, expert, vt * 16 + q * 8 + half * 4);
+      }
+    }
+  }
+}
+
+template <int WM, int WN, int TM, int TN, int NS, bool MOE>
+hipError_t launch_tile(const I8Args& a, bool silu, int m_blocks, hipStream_t s) {
+  constexpr int BN = 32 * TN * WN, THREADS = 64 * WM * WN;
+  const int tiles = (a.cols + 15) / 16 * (silu ? 2 : 1);
+  const int n_blocks = (tiles + BN / 16 - 1) / (BN / 16);
+  const int64_t blocks = (int64_t)(MOE ? moe_grid_blocks(m_blocks) : m_blocks) * n_blocks;
+  if (blocks * THREADS >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(THREADS), 0, s, a, m_blocks, n_blocks);
+    return hipGetLastError();
+  };
+  if (silu)
+    return a.a_zeros ? go(gemm_i8_tile_kernel<WM, WN, TM, TN, NS, true, true, MOE>)
+                     : go(gemm_i8_tile_kernel<WM, WN, TM, TN, NS, true, false, MOE>);
+  return a.a_zeros ? go(gemm_i8_tile_kernel<WM, WN, TM, TN, NS, false, true, MOE>)
+                   : go(gemm_i8_tile_kernel<WM, WN, TM, TN, NS, false, false, MOE>);
+}
+
 }  // namespace
 
 int gemm_i8_split(int64_t M, int64_t n, int64_t k, bool silu) { return 1; }
@@ -267,8 +514,12 @@ hipError_t launch_gemm_i8(const I8Args& a, bool silu, int split, hipStream_t s) 
     e = launch_rows<1, 2, 8, false>(a, silu, 1, split, s);
   else if (a.M <= 32)
     e = launch_rows<2, 2, 8, false>(a, silu, 1, split, s);
+  else if (a.M <= 64)
+    e = launch_rows<4, 2, 8, false>(a, silu, 1, split, s);
+  else if (a.M <= 1024)
+    return launch_tile<2, 4, 2, 1, 3, false>(a, silu, (a.M + 127) / 128, s);
   else
-    e = launch_rows<4, 2, 8, false>(a, silu, (a.M + 63) / 64, split, s);
+    return launch_tile<2, 4, 4, 2, 2, false>(a, silu, (a.M + 255) / 256, s);
   if (e != hipSuccess || split <= 1) return e;
   const int64_t threads = (int64_t)a.M * ((a.cols + 3) / 4);
   const dim3 grid((unsigned)((threads + 255) / 256));
@@ -283,8 +534,8 @@ hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int block_m, int m_blo
   switch (block_m) {
     case 16: return launch_rows<1, 2, 8, true>(a, silu, m_blocks, 1, s);
     case 32: return launch_rows<2, 2, 8, true>(a, silu, m_blocks, 1, s);
-    case 64: return launch_rows<4, 2, 8, true>(a, silu, m_blocks, 1, s);
-    case 128: return launch_rows<8, 2, 4, true>(a, silu, m_blocks, 1, s);
+    case 64: return launch_tile<2, 4, 1, 2, 3, true>(a, silu, m_blocks, s);
+    case 128: return launch_tile<2, 4, 2, 2, 3, true>(a, silu, m_blocks, s);
     default: return hipErrorInvalidValue;
   }
 }
