@@ -30,6 +30,7 @@ qdg_status hip_status(hipError_t e, const char* what) {
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int64_t kMaxStride = (int64_t)1 << 28;  // eight rows within 32-bit offsets
 constexpr int64_t kMaxSide = (int64_t)1 << 26;  // rows and columns of the int8 products: launches stay within 2^32 threads
 
 // The checks that the dense and the grouped product share.
@@ -52,6 +53,7 @@ qdg_status check_i8(const qdg_i8_config* c) {
   const int64_t cols = c->epilogue == QDG_EPI_SILU_MUL ? c->n / 2 : c->n;
   if (c->lda < c->k || c->ldb < c->k || c->ldy < cols)
     return fail(QDG_ERR_INVALID_ARG, "a row stride is shorter than its row");
+  if (c->lda > kMaxStride || c->ldb > kMaxStride) return fail(QDG_ERR_UNSUPPORTED, "lda and ldb must be at most 2^28");
   if (c->lda % 16 || c->ldb % 16) return fail(QDG_ERR_MISALIGNED, "lda and ldb must be multiples of 16 bytes");
   return QDG_OK;
 }

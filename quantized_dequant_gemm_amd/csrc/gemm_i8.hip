@@ -274,19 +274,37 @@ __device__ __forceinline__ i32x16_t mfma_i8_32(u32x4_t a, u32x4_t b, i32x16_t c)
 
 __device__ __forceinline__ int i8_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
-// The copies of group g into one stage: every wave issues the same number.
-// Chunks behind the row's end read the row's last chunk instead (masked
-// before use).
-template <int BM, int BN, int NW, int TAG>
-__device__ __forceinline__ void i8_load_stage(char* st, const int8_t* const (&src)[(BM + BN) / 8 / NW], int wave,
-                                              int lane, int g, int last_chunk) {
+// Where a wave's copies read: copy q takes 8 rows of A or B through a buffer
+// resource that starts at the first of them and ends with the operand, so
+// that rows and bytes behind the operand's end read as 0 without a branch
+// (bytes between a row's end and its stride are masked before use). off: the
+// lane's row and chunk.
+template <int LOADS>
+struct I8Src {
+  __amdgpu_buffer_rsrc_t rsrc[LOADS];
+  uint32_t off[LOADS];
+};
+
+// The resource for rows from `row` on of an operand of `rows` rows, its last
+// row `len` bytes long.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t i8_rows_rsrc(const int8_t* base, int64_t row, int64_t rows,
+                                                              int64_t ld, int64_t len) {
+  int64_t left = (rows - 1 - row) * ld + len;
+  left = left < 0 ? 0 : left > 0xFFFFFFFFll ? 0xFFFFFFFFll : left;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base + (left > 0 ? row * ld : 0)), (short)0,
+                                           (int)(uint32_t)left, 0x00020000);
+}
+
+// Copies FROM .. TO - 1 of group g into one stage (every wave issues the same
+// number). Buffer loads, because the compiler tracks them apart from LDS
+// reads; a global load to LDS in flight makes it wait for every LDS read
+// where one would do.
+template <int FROM, int TO, int LOADS, int NW, int TAG>
+__device__ __forceinline__ void i8_load_stage(char* st, const I8Src<LOADS>& src, int wave, int g) {
 #pragma unroll
-  for (int q = 0; q < (BM + BN) / 8 / NW; ++q) {
-    const int i = q * NW + wave;  // rows 8 i .. 8 i + 7 of the stage
-    const int ch = (lane & 7) ^ (lane >> 3) ^ (i & 1);
-    const uint32_t off = (uint32_t)min(g * 8 + ch, last_chunk) * 16u;
-    __builtin_amdgcn_global_load_lds(src[q] + off, (lds_void*)(st + i * 1024), 16, 0, 0);
-  }
+  for (int q = FROM; q < TO; ++q)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src.rsrc[q], (lds_void*)(st + (q * NW + wave) * 1024), 16,
+                                             src.off[q] + (uint32_t)g * 128u, 0, 0, 0);
 }
 
 // Zeroes the bytes from k on of the 16 at byte kk of a row.
@@ -299,32 +317,89 @@ __device__ __forceinline__ u32x4_t i8_mask(u32x4_t v, int kk, int k) {
   return v;
 }
 
-// One group of a wave's (32 TM) x (32 TN) tile.
-template <int TM, int TN, bool ZP, bool MASK, int TAG>
-__device__ __forceinline__ void i8_group(const char* st, int a_lane, int b_lane, int sw, int half, int kk, int k,
-                                         i32x16_t (&acc)[TM][TN], int (&zs)[TN]) {
+// The fragments of one 32-byte step of a wave's (32 TM) x (32 TN) tile.
+template <int TM, int TN>
+struct I8Frag {
+  u32x4_t a[TM], b[TN];
+};
+
+template <int TM, int TN>
+__device__ __forceinline__ void i8_frag_load(I8Frag<TM, TN>& f, const char* st, int a_lane, int b_lane, int at) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int at = ((2 * s + half) ^ sw) * 16;
-    u32x4_t a[TM], b[TN];
+  for (int t = 0; t < TN; ++t) f.b[t] = *(const u32x4_t*)(st + b_lane + t * 4096 + at);
 #pragma unroll
-    for (int t = 0; t < TN; ++t) b[t] = *(const u32x4_t*)(st + b_lane + t * 4096 + at);
+  for (int t = 0; t < TM; ++t) f.a[t] = *(const u32x4_t*)(st + a_lane + t * 4096 + at);
+}
+
+// kk: the row byte that the lane's chunk holds (bytes from k on count 0).
+template <int TM, int TN>
+__device__ __forceinline__ void i8_frag_mask(I8Frag<TM, TN>& f, int kk, int k) {
 #pragma unroll
-    for (int t = 0; t < TM; ++t) a[t] = *(const u32x4_t*)(st + a_lane + t * 4096 + at);
-    if constexpr (MASK) {
-      const int at_k = kk + (2 * s + half) * 16;
+  for (int t = 0; t < TN; ++t) f.b[t] = i8_mask(f.b[t], kk, k);
 #pragma unroll
-      for (int t = 0; t < TN; ++t) b[t] = i8_mask(b[t], at_k, k);
+  for (int t = 0; t < TM; ++t) f.a[t] = i8_mask(f.a[t], kk, k);
+}
+
+// MFMAs FROM .. TO - 1 of the step's TM * TN.
+template <int FROM, int TO, int TM, int TN, bool ZP, int TAG>
+__device__ __forceinline__ void i8_frag_mma(const I8Frag<TM, TN>& f, i32x16_t (&acc)[TM][TN], int (&zs)[TN]) {
 #pragma unroll
-      for (int t = 0; t < TM; ++t) a[t] = i8_mask(a[t], at_k, k);
-    }
-#pragma unroll
-    for (int t = 0; t < TN; ++t) {
-      if constexpr (ZP) zs[t] = i8_sum16(b[t], zs[t]);
-#pragma unroll
-      for (int m = 0; m < TM; ++m) acc[m][t] = mfma_i8_32(b[t], a[m], acc[m][t]);
-    }
+  for (int i = FROM; i < TO; ++i) {
+    const int t = i / TM, m = i % TM;
+    if (ZP && m == 0) zs[t] = i8_sum16(f.b[t], zs[t]);
+    acc[m][t] = mfma_i8_32(f.b[t], f.a[m], acc[m][t]);
   }
+}
+
+// The first half of a step's MFMAs with the copies of a group between them.
+template <int I, int H, int LOADS, int NW, int TM, int TN, bool ZP, int TAG>
+__device__ __forceinline__ void i8_mma_and_load(const I8Frag<TM, TN>& f, i32x16_t (&acc)[TM][TN], int (&zs)[TN],
+                                                char* st, const I8Src<LOADS>& src, int wave, int g) {
+  if constexpr (I < H) {
+    i8_frag_mma<I, I + 1, TM, TN, ZP, TAG + I>(f, acc, zs);
+    i8_load_stage<LOADS * I / H, LOADS*(I + 1) / H, LOADS, NW, TAG>(st, src, wave, g);
+    __builtin_amdgcn_sched_barrier(0);
+    i8_mma_and_load<I + 1, H, LOADS, NW, TM, TN, ZP, TAG>(f, acc, zs, st, src, wave, g);
+  }
+}
+
+// Group g of the K loop. Its first fragments are in f0 already. Each step's
+// fragment reads go out before the MFMAs of the step before; the barrier sits
+// in front of the last step's MFMAs, where every wave has its last fragments
+// of this group in registers: then the next group's first reads and the
+// copies of group g + NS into this group's stage run under those MFMAs.
+// LEFT: copies that may stay in flight while the next group's have landed.
+template <int LOADS, int NW, int TM, int TN, int LEFT, bool ZP, bool MASK, int TAG>
+__device__ __forceinline__ void i8_group(char* st, const char* next, const I8Src<LOADS>& src, int wave, int g,
+                                         int load_g, int a_lane, int b_lane, const int (&at)[4], int half, int k,
+                                         I8Frag<TM, TN>& f0, I8Frag<TM, TN>& f1, i32x16_t (&acc)[TM][TN],
+                                         int (&zs)[TN]) {
+  constexpr int MF = TM * TN, H = MF / 2;
+  const int kk = g * 128 + half * 16;
+  i8_frag_load(f1, st, a_lane, b_lane, at[1]);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (MASK) i8_frag_mask(f0, kk, k);
+  i8_frag_mma<0, MF, TM, TN, ZP, TAG>(f0, acc, zs);
+  __builtin_amdgcn_sched_barrier(0);
+  i8_frag_load(f0, st, a_lane, b_lane, at[2]);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (MASK) i8_frag_mask(f1, kk + 32, k);
+  i8_frag_mma<0, MF, TM, TN, ZP, TAG>(f1, acc, zs);
+  __builtin_amdgcn_sched_barrier(0);
+  i8_frag_load(f1, st, a_lane, b_lane, at[3]);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (MASK) i8_frag_mask(f0, kk + 64, k);
+  i8_frag_mma<0, MF, TM, TN, ZP, TAG>(f0, acc, zs);
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | (7 << 4) | (15 << 8) | ((LEFT >> 4) << 14));
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+  if constexpr (MASK) i8_frag_mask(f1, kk + 96, k);
+  i8_mma_and_load<0, H, LOADS, NW, TM, TN, ZP, TAG>(f1, acc, zs, st, src, wave, load_g);
+  i8_frag_load(f0, next, a_lane, b_lane, at[0]);
+  __builtin_amdgcn_sched_barrier(0);
+  i8_frag_mma<H, MF, TM, TN, ZP, TAG + 64>(f1, acc, zs);
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int WM, int WN, int TM, int TN, int NS, bool SILU, bool ZP, bool MOE>
@@ -370,27 +445,34 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   // 16-column tiles of B in the order the epilogue wants (gate and up tiles
   // alternate with SILU)
   const int vt0 = nb * (BN / 16);
-  const int8_t* src[LOADS];
+  I8Src<LOADS> src;
+  const int64_t k16 = (p.k + 15) / 16 * 16;
 #pragma unroll
   for (int q = 0; q < LOADS; ++q) {
-    const int row = (q * NW + wave) * 8 + (lane >> 3);  // stage row: A, then B
-    if (row < BM) {
-      const int grow = mb * BM + row;
-      int ar = min(grow, p.M - 1);
+    const int i = q * NW + wave;  // rows 8 i .. 8 i + 7 of the stage: A, then B
+    const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3) ^ (i & 1)) * 16u;
+    if (i < BM / 8) {
       if constexpr (MOE) {
-        const int id = p.sorted_ids[grow];
-        ar = (unsigned)id < (unsigned)p.num_pairs ? (p.a_per_pair ? id : id / p.top_k) : 0;
+        const int id = p.sorted_ids[mb * BM + i * 8 + (lane >> 3)];
+        const int ar = (unsigned)id < (unsigned)p.num_pairs ? (p.a_per_pair ? id : id / p.top_k) : 0;
+        src.rsrc[q] = i8_rows_rsrc(p.A, 0, p.M, p.lda, k16);  // at most 4 GiB (checked by the host)
+        src.off[q] = (uint32_t)ar * (uint32_t)p.lda + chunk;
+      } else {
+        src.rsrc[q] = i8_rows_rsrc(p.A, mb * BM + i * 8, p.M, p.lda, k16);
+        src.off[q] = (uint32_t)(lane >> 3) * (uint32_t)p.lda + chunk;
       }
-      src[q] = p.A + (int64_t)ar * p.lda;
     } else {
+      const int row = i * 8 - BM;
       int first, rows;
-      i8_tile<SILU>(p, vt0 + (row - BM) / 16, first, rows);
-      // tiles behind the layer read row 0; their results are never stored
-      const int br = rows > 0 ? first + min((row - BM) % 16, rows - 1) : 0;
-      src[q] = p.B + ((int64_t)expert * p.n + br) * p.ldb;
+      i8_tile<SILU>(p, vt0 + row / 16, first, rows);
+      // rows behind a tile's last column are other rows of B or zeros, their
+      // results are never stored
+      src.rsrc[q] = i8_rows_rsrc(p.B + (int64_t)expert * p.n * p.ldb, rows > 0 ? first + row % 16 : p.n, p.n, p.ldb,
+                                 k16);
+      src.off[q] = (uint32_t)(lane >> 3) * (uint32_t)p.ldb + chunk;
     }
   }
-  const int groups = (p.k + 127) / 128, last_chunk = (p.k - 1) / 16;
+  const int groups = (p.k + 127) / 128;
   const int a_lane = (wm * TM * 32 + r) * 128, b_lane = (BM + wn * TN * 32 + r) * 128, sw = i8_swizzle(r);
   i32x16_t acc[TM][TN];
   int zs[TN];
@@ -402,40 +484,33 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][t][i] = 0;
   }
+  int at[4];
 #pragma unroll
-  for (int q = 0; q < NS - 1; ++q)
-    i8_load_stage<BM, BN, NW, TAG>(stage[q], src, wave, lane, min(q, groups - 1), last_chunk);
+  for (int q = 0; q < 4; ++q) at[q] = ((2 * q + half) ^ sw) * 16;
+#pragma unroll
+  for (int q = 0; q < NS; ++q)
+    i8_load_stage<0, LOADS, LOADS, NW, TAG>(stage[q], src, wave, min(q, groups - 1));
+  constexpr int LEFT = LOADS * (NS - 1);
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | (7 << 4) | (15 << 8) | ((LEFT >> 4) << 14));
+  asm volatile("s_barrier" ::: "memory");
+  I8Frag<TM, TN> f0, f1;
+  i8_frag_load(f0, st0, a_lane, b_lane, at[0]);
   const int full = p.k / 128;  // groups that need no mask
   int g = 0;
   for (; g + NS <= full; g += NS) {
 #pragma unroll
-    for (int cur = 0; cur < NS; ++cur) {
-      // this wave's copies of group g + cur have landed; those of the NS - 2
-      // groups behind it stay in flight
-      constexpr int LEFT = LOADS * (NS - 2);
-      __builtin_amdgcn_s_waitcnt((LEFT & 15) | (7 << 4) | (15 << 8) | ((LEFT >> 4) << 14));
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-      asm volatile("s_barrier" ::: "memory");
-      i8_load_stage<BM, BN, NW, TAG + 65536>(stage[(cur + NS - 1) % NS], src, wave, lane,
-                                             min(g + cur + NS - 1, groups - 1), last_chunk);
-      i8_group<TM, TN, ZP, false, TAG>(stage[cur], a_lane, b_lane, sw, half, 0, 0, acc, zs);
-    }
+    for (int cur = 0; cur < NS; ++cur)
+      i8_group<LOADS, NW, TM, TN, LOADS*(NS - 2), ZP, false, TAG + (1 << 16)>(
+          stage[cur], stage[(cur + 1) % NS], src, wave, g + cur, min(g + cur + NS, groups - 1), a_lane, b_lane, at,
+          half, p.k, f0, f1, acc, zs);
   }
-  // the remaining groups, the last one cut at k: copies for the first NS - 1
-  // of them are in flight
-#pragma unroll 1
-  for (; g < groups; g += NS) {
+  // the remaining groups, the last one cut at k
 #pragma unroll
-    for (int cur = 0; cur < NS; ++cur) {
-      if (g + cur < groups) {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        i8_load_stage<BM, BN, NW, TAG + 131072>(stage[(cur + NS - 1) % NS], src, wave, lane,
-                                                min(g + cur + NS - 1, groups - 1), last_chunk);
-        i8_group<TM, TN, ZP, true, TAG>(stage[cur], a_lane, b_lane, sw, half, (g + cur) * 128, p.k, acc, zs);
-      }
-    }
-  }
+  for (int cur = 0; cur < NS; ++cur)
+    if (g + cur < groups)
+      i8_group<LOADS, NW, TM, TN, 0, ZP, true, TAG + (1 << 17)>(
+          stage[cur], stage[(cur + 1) % NS], src, wave, g + cur, groups - 1, a_lane, b_lane, at, half, p.k, f0, f1,
+          acc, zs);
   __builtin_amdgcn_s_waitcnt(0);  // the trailing copies have landed
   __syncthreads();
 
@@ -531,6 +606,10 @@ hipError_t launch_gemm_i8(const I8Args& a, bool silu, int split, hipStream_t s) 
 }
 
 hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int block_m, int m_blocks, hipStream_t s) {
+  // the tiles address A with 32 bits
+  const bool far = (int64_t)a.M * a.lda > (int64_t)0xFFFF0000;
+  if (far && block_m == 64) return launch_rows<4, 2, 8, true>(a, silu, m_blocks, 1, s);
+  if (far && block_m == 128) return launch_rows<8, 2, 4, true>(a, silu, m_blocks, 1, s);
   switch (block_m) {
     case 16: return launch_rows<1, 2, 8, true>(a, silu, m_blocks, 1, s);
     case 32: return launch_rows<2, 2, 8, true>(a, silu, m_blocks, 1, s);
