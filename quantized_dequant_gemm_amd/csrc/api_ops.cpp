@@ -83,7 +83,7 @@ qdg_status i8_args(const qdg_i8_config* c, const int8_t* A, const float* a_scale
   a.k = (int)c->k;
   a.cols = (int)(c->epilogue == QDG_EPI_SILU_MUL ? c->n / 2 : c->n);
   a.otype = c->otype;
-  a.y_vec = aligned(Y, 4 * esz) && c->ldy % 4 == 0;
+  a.y_vec = aligned(Y, 16) && c->ldy * esz % 16 == 0;
   a.num_experts = c->num_experts;
   *out = a;
   return QDG_OK;

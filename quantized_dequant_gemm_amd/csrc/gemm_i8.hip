@@ -22,6 +22,19 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, int vt, int& first, int
   rows = p.cols - j;
 }
 
+// One form in every kernel, so that a row does not depend on which one ran.
+__device__ __forceinline__ float i8_scale(int acc, float sa, float sb, float bias) {
+  return __builtin_fmaf((float)acc * sa, sb, bias);
+}
+
+__device__ __forceinline__ float i8_silu(float x) { return x / (1.0f + expf(-x)); }
+
+// Four values to bf16 (v_cvt_pk_bf16_f32: nearest even).
+__device__ __forceinline__ u32x2_t i8_bf16x4(f32x4_t v) {
+  typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4_t;
+  return __builtin_bit_cast(u32x2_t, __builtin_convertvector(v, bf16x4_t));
+}
+
 // Four consecutive outputs of one row: the integer sums (gate and up with
 // SILU) of columns j0 .. j0 + 3 through scales, bias, epilogue and rounding.
 template <bool SILU>
@@ -39,25 +52,21 @@ __device__ __forceinline__ void i8_finish(const I8Args& p, i32x4_t g, i32x4_t u,
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t c = col + min(i, cnt - 1);
-      float y = (float)g[i] * sa * p.b_scales[c];
-      if (p.bias) y += p.bias[c];
+      float y = i8_scale(g[i], sa, p.b_scales[c], p.bias ? p.bias[c] : 0.f);
       if constexpr (SILU) {
-        float v = (float)u[i] * sa * p.b_scales[c + p.cols];
-        if (p.bias) v += p.bias[c + p.cols];
-        y = y / (1.0f + expf(-y)) * v;
+        y = i8_silu(y) * i8_scale(u[i], sa, p.b_scales[c + p.cols], p.bias ? p.bias[c + p.cols] : 0.f);
       }
       out[i] = __builtin_bit_cast(uint32_t, y);
     }
   }
   if (p.otype == QDG_O_BF16) {
     uint16_t* dst = (uint16_t*)p.Y + yrow * p.ldy + j0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = f32_to_bf16_rne(__builtin_bit_cast(float, out[i]));
+    const u32x2_t h = i8_bf16x4(__builtin_bit_cast(f32x4_t, u32x4_t{out[0], out[1], out[2], out[3]}));
     if (cnt == 4 && p.y_vec) {
-      *(u32x2_t*)dst = u32x2_t{out[0] | out[1] << 16, out[2] | out[3] << 16};
+      *(u32x2_t*)dst = h;
     } else {
       for (int i = 0; i < 4; ++i)
-        if (i < cnt) dst[i] = (uint16_t)out[i];
+        if (i < cnt) dst[i] = (uint16_t)(h[i >> 1] >> (16 * (i & 1)));
     }
   } else {
     uint32_t* dst = (uint32_t*)p.Y + yrow * p.ldy + j0;
@@ -514,48 +523,111 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   __builtin_amdgcn_s_waitcnt(0);  // the trailing copies have landed
   __syncthreads();
 
-  // column sums of B into the order of the result's rows
-  int* zbuf = (int*)st0 + wave * TN * 32;
+  // ---- epilogue. A lane holds row r of each 32-row tile and, of each
+  // 32-column tile, the columns 8 q + 4 half .. + 3. Column scales and biases
+  // (in the order of the tile's columns) and the column sums of B go through
+  // LDS; so does each strip of 32 rows, so that stores are whole row segments.
+  constexpr int PITCH = 128 + 16, STRIP = 32 * PITCH;  // a strip row: at most 128 bytes
+  static_assert(NW / 2 * STRIP + BN * 8 + NW * TN * 128 <= BYTES, "the epilogue's buffers fit a stage");
+  float* cscale = (float*)(st1 + NW / 2 * STRIP);
+  float* cbias = cscale + BN;
+  int* zbuf = (int*)(cbias + BN) + wave * TN * 32;
+  char* strip = (wave < NW / 2 ? st0 : st1) + wave % (NW / 2) * STRIP;
+  const bool raw = p.otype == QDG_O_I32;
+  if (!raw)
+    for (int c = threadIdx.x; c < BN; c += 64 * NW) {
+      int first, rows;
+      i8_tile<SILU>(p, vt0 + c / 16, first, rows);
+      const int64_t at = (int64_t)expert * p.n + (rows > 0 ? first + min(c % 16, rows - 1) : 0);
+      cscale[c] = p.b_scales[at];
+      cbias[c] = p.bias ? p.bias[at] : 0.f;
+    }
   if constexpr (ZP) {
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
       const int z = zs[t] + __shfl_xor(zs[t], 32);
       if (half == 0) zbuf[t * 32 + r] = z;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   }
-  // a lane holds row r of each 32-row tile and, of each 32-column tile, the
-  // columns 8 q + 4 half .. + 3
+  __syncthreads();
+  constexpr int TC = SILU ? 16 : 32;  // columns of Y from a 32-column tile
+  const int wave_col = (vt0 * 16 + wn * TN * 32) / (SILU ? 2 : 1);
 #pragma unroll
   for (int m = 0; m < TM; ++m) {
     const int grow = mb * BM + (wm * TM + m) * 32 + r;
-    int yr = grow, ar = grow;
+    int yr = grow, ar = min(grow, p.M - 1);
     bool real = grow < p.M;
     if constexpr (MOE) {
       yr = p.sorted_ids[grow];
       real = (unsigned)yr < (unsigned)p.num_pairs;
-      ar = p.a_per_pair ? yr : yr / p.top_k;
+      ar = !real ? 0 : p.a_per_pair ? yr : yr / p.top_k;
     }
-    if (!real) continue;
+    yr = real ? yr : -1;
     const int za = ZP ? p.a_zeros[ar] : 0;
+    const float sa = raw ? 1.f : p.a_scales[ar];
+    auto sums = [&](int t, int q) {
+      i32x4_t v;
+      i32x4_t z = {0, 0, 0, 0};
+      if constexpr (ZP) z = *(const i32x4_t*)(zbuf + t * 32 + q * 8 + half * 4);
 #pragma unroll
-    for (int t = 0; t < TN; ++t) {
-      i32x4_t v[4];
+      for (int i = 0; i < 4; ++i) v[i] = acc[m][t][q * 4 + i] - za * z[i];
+      return v;
+    };
+    auto scaled = [&](int t, int q) {
+      const int c = (wn * TN + t) * 32 + q * 8 + half * 4;
+      const f32x4_t cs = *(const f32x4_t*)(cscale + c), cb = *(const f32x4_t*)(cbias + c);
+      const i32x4_t v = sums(t, q);
+      f32x4_t y;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        i32x4_t z = {0, 0, 0, 0};
-        if constexpr (ZP) z = *(const i32x4_t*)(zbuf + t * 32 + q * 8 + half * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[q][i] = acc[m][t][q * 4 + i] - za * z[i];
-      }
-      const int vt = vt0 + (wn * TN + t) * 2;  // two 16-column tiles of B
+      for (int i = 0; i < 4; ++i) y[i] = i8_scale(v[i], sa, cs[i], cb[i]);
+      return y;
+    };
+    auto out4 = [&](int t, int q) {  // columns 8 q + 4 half .. + 3 of tile t's TC
+      if (raw) return __builtin_bit_cast(f32x4_t, sums(t, q));
+      f32x4_t y = scaled(t, q);
       if constexpr (SILU) {
+        const f32x4_t u = scaled(t, q + 2);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) i8_finish<SILU>(p, v[q], v[q + 2], yr, ar, expert, vt * 8 + q * 8 + half * 4);
-      } else {
+        for (int i = 0; i < 4; ++i) y[i] = i8_silu(y[i]) * u[i];
+      }
+      return y;
+    };
+    // the strip's rows of `cols` columns of es bytes out, from column c0 on
+    auto flush = [&](int c0, int cols, int es) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const int per = cols * es / 16;  // 16-byte pieces of a row
 #pragma unroll
-        for (int q = 0; q < 4; ++q) i8_finish<SILU>(p, v[q], v[q], yr, ar, expert, vt * 16 + q * 8 + half * 4);
+      for (int i = lane; i < 32 * per; i += 64) {
+        const int row = i / per, piece = i % per;
+        const int y = __shfl(yr, row), j = c0 + piece * (16 / es);
+        const u32x4_t v = *(const u32x4_t*)(strip + row * PITCH + piece * 16);
+        if (y < 0 || j >= p.cols) continue;
+        char* dst = (char*)p.Y + ((int64_t)y * p.ldy + j) * es;
+        if (p.y_vec && j + 16 / es <= p.cols) {
+          *(u32x4_t*)dst = v;
+        } else if (es == 4) {
+          for (int e = 0; e < 4 && j + e < p.cols; ++e) ((uint32_t*)dst)[e] = v[e];
+        } else {
+          for (int e = 0; e < 8 && j + e < p.cols; ++e) ((uint16_t*)dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    };
+    if (p.otype == QDG_O_BF16) {
+#pragma unroll
+      for (int t = 0; t < TN; ++t)
+#pragma unroll
+        for (int q = 0; q < TC / 8; ++q)
+          *(u32x2_t*)(strip + r * PITCH + (t * TC + q * 8 + half * 4) * 2) = i8_bf16x4(out4(t, q));
+      flush(wave_col, TN * TC, 2);
+    } else {
+#pragma unroll
+      for (int t = 0; t < TN; ++t) {
+#pragma unroll
+        for (int q = 0; q < TC / 8; ++q) *(f32x4_t*)(strip + r * PITCH + (q * 8 + half * 4) * 4) = out4(t, q);
+        flush(wave_col + t * TC, TC, 4);
       }
     }
   }

@@ -174,7 +174,7 @@ struct I8Args {
   int M, n, k;             // M: rows of A (dense)
   int cols;                // columns of Y (n, or n / 2 with the SiLU*mul epilogue)
   int otype;
-  int y_vec;               // Y rows allow stores of four elements at a time
+  int y_vec;               // Y rows are 16-byte aligned
   int32_t* partial;        // split K: int32 partials [split][M][n]
   // grouped by expert (sorted_ids NULL: dense)
   const int32_t* sorted_ids;
