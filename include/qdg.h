@@ -630,7 +630,8 @@ qdg_status qdg_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const float* a
    i / top_k (a_per_pair = 0). a_scales and a_zeros are indexed by r,
    b_scales and bias are f32 [num_experts][n]. Rows without a real entry stay
    as they were. block_m in {16, 32, 64, 128}: the smaller while experts hold
-   few rows each. T*top_k <= 2^20. No workspace. */
+   few rows each. T*top_k <= 2^20; A at most 3.75 GiB (its rows times lda; else
+   QDG_ERR_UNSUPPORTED). No workspace. */
 qdg_status qdg_moe_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const float* a_scales, const int32_t* a_zeros,
                            const int8_t* B, const float* b_scales, const float* bias, const int32_t* sorted_ids,
                            const int32_t* block_expert, const int32_t* num_padded, int64_t T, int32_t top_k,

@@ -82,16 +82,18 @@ qdg_status i8_args(const qdg_i8_config* c, const int8_t* A, const float* a_scale
   a.n = (int)c->n;
   a.k = (int)c->k;
   a.cols = (int)(c->epilogue == QDG_EPI_SILU_MUL ? c->n / 2 : c->n);
+  a.vcols = (int)gemm_i8_vcols(a.cols, c->epilogue == QDG_EPI_SILU_MUL);
   a.otype = c->otype;
-  a.y_vec = aligned(Y, 16) && c->ldy * esz % 16 == 0;
   a.num_experts = c->num_experts;
   *out = a;
   return QDG_OK;
 }
 
-size_t i8_workspace(const qdg_i8_config* c, int64_t M, int* split) {
-  *split = M > 0 ? gemm_i8_split(M, c->n, c->k, c->epilogue == QDG_EPI_SILU_MUL) : 1;
-  return *split > 1 ? (size_t)*split * (size_t)M * (size_t)c->n * sizeof(int32_t) : 0;
+size_t i8_workspace(const qdg_i8_config* c, int64_t M) {
+  const bool silu = c->epilogue == QDG_EPI_SILU_MUL;
+  const int64_t vcols = gemm_i8_vcols(silu ? c->n / 2 : c->n, silu);
+  const int split = M > 0 ? gemm_i8_split(M, vcols, c->k, silu) : 1;
+  return split > 1 ? (size_t)split * (size_t)M * (size_t)vcols * sizeof(int32_t) : 0;
 }
 
 }  // namespace
@@ -155,8 +157,7 @@ qdg_status qdg_gemm_i8_workspace(const qdg_i8_config* cfg, int64_t M, size_t* by
   if (cfg->num_experts != 1) return fail(QDG_ERR_INVALID_ARG, "the dense product has one expert");
   if (M < 0) return fail(QDG_ERR_INVALID_ARG, "M < 0");
   if (M > kMaxSide) return fail(QDG_ERR_UNSUPPORTED, "M must be at most 2^26");
-  int split;
-  *bytes = i8_workspace(cfg, M, &split);
+  *bytes = i8_workspace(cfg, M);
   return QDG_OK;
 }
 
@@ -173,15 +174,14 @@ qdg_status qdg_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const float* a
   st = i8_args(cfg, A, a_scales, a_zeros, B, b_scales, bias, Y, &a);
   if (st != QDG_OK) return st;
   a.M = (int)M;
-  int split;
-  const size_t need = i8_workspace(cfg, M, &split);
+  const size_t need = i8_workspace(cfg, M);
   if (need > 0) {
     if (!workspace || ws_bytes < need)
       return fail(QDG_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace ? ws_bytes : 0, need);
     if (!aligned(workspace, 16)) return fail(QDG_ERR_MISALIGNED, "workspace must be 16-byte aligned");
     a.partial = (int32_t*)workspace;
   }
-  return hip_status(launch_gemm_i8(a, cfg->epilogue == QDG_EPI_SILU_MUL, split, (hipStream_t)stream),
+  return hip_status(launch_gemm_i8(a, cfg->epilogue == QDG_EPI_SILU_MUL, (hipStream_t)stream),
                     "gemm_i8 launch");
 }
 
@@ -208,7 +208,10 @@ qdg_status qdg_moe_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const floa
   a.num_pairs = (int)(T * top_k);
   a.top_k = top_k;
   a.a_per_pair = a_per_pair ? 1 : 0;
-  return hip_status(launch_moe_gemm_i8(a, cfg->epilogue == QDG_EPI_SILU_MUL, block_m, (int)(capacity / block_m),
+  a.block_m = block_m;
+  if ((int64_t)a.M * a.lda > (int64_t)kI8FarRow)
+    return fail(QDG_ERR_UNSUPPORTED, "A is longer than 3.75 GiB: route fewer tokens at a time");
+  return hip_status(launch_moe_gemm_i8(a, cfg->epilogue == QDG_EPI_SILU_MUL, (int)(capacity / block_m),
                                        (hipStream_t)stream),
                     "moe_gemm_i8 launch");
 }

@@ -6,7 +6,6 @@
 // The weights are the MFMA's row operand, so a lane of the result holds four
 // consecutive columns of one row of Y. With the SiLU*mul epilogue the 16-column tiles
 // of B alternate between gate and up rows, so that a lane holds both halves.
-#include <algorithm>
 
 #include "qdg_device.h"
 #include "qdg_internal.h"
@@ -35,11 +34,14 @@ __device__ __forceinline__ u32x2_t i8_bf16x4(f32x4_t v) {
   return __builtin_bit_cast(u32x2_t, __builtin_convertvector(v, bf16x4_t));
 }
 
+// Stores of vectors at any element (gfx950 takes them unaligned).
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
+
 // Four consecutive outputs of one row: the integer sums (gate and up with
 // SILU) of columns j0 .. j0 + 3 through scales, bias, epilogue and rounding.
 template <bool SILU>
-__device__ __forceinline__ void i8_finish(const I8Args& p, i32x4_t g, i32x4_t u, int64_t yrow, int arow, int expert,
-                                          int j0) {
+__device__ __forceinline__ void i8_finish(const I8Args& p, i32x4_t g, i32x4_t u, int yrow, int arow, int j0) {
   if (j0 >= p.cols) return;
   const int cnt = min(4, p.cols - j0);
   uint32_t out[4];
@@ -48,10 +50,9 @@ __device__ __forceinline__ void i8_finish(const I8Args& p, i32x4_t g, i32x4_t u,
     for (int i = 0; i < 4; ++i) out[i] = (uint32_t)g[i];
   } else {
     const float sa = p.a_scales[arow];
-    const int64_t col = (int64_t)expert * p.n + j0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t c = col + min(i, cnt - 1);
+      const int c = j0 + min(i, cnt - 1);
       float y = i8_scale(g[i], sa, p.b_scales[c], p.bias ? p.bias[c] : 0.f);
       if constexpr (SILU) {
         y = i8_silu(y) * i8_scale(u[i], sa, p.b_scales[c + p.cols], p.bias ? p.bias[c + p.cols] : 0.f);
@@ -60,18 +61,18 @@ __device__ __forceinline__ void i8_finish(const I8Args& p, i32x4_t g, i32x4_t u,
     }
   }
   if (p.otype == QDG_O_BF16) {
-    uint16_t* dst = (uint16_t*)p.Y + yrow * p.ldy + j0;
+    uint16_t* dst = (uint16_t*)p.Y + (int64_t)yrow * p.ldy + j0;
     const u32x2_t h = i8_bf16x4(__builtin_bit_cast(f32x4_t, u32x4_t{out[0], out[1], out[2], out[3]}));
-    if (cnt == 4 && p.y_vec) {
-      *(u32x2_t*)dst = h;
+    if (cnt == 4) {
+      *(u32x2_any_t*)dst = h;
     } else {
       for (int i = 0; i < 4; ++i)
         if (i < cnt) dst[i] = (uint16_t)(h[i >> 1] >> (16 * (i & 1)));
     }
   } else {
-    uint32_t* dst = (uint32_t*)p.Y + yrow * p.ldy + j0;
-    if (cnt == 4 && p.y_vec) {
-      *(u32x4_t*)dst = u32x4_t{out[0], out[1], out[2], out[3]};
+    uint32_t* dst = (uint32_t*)p.Y + (int64_t)yrow * p.ldy + j0;
+    if (cnt == 4) {
+      *(u32x4_any_t*)dst = u32x4_t{out[0], out[1], out[2], out[3]};
     } else {
       for (int i = 0; i < 4; ++i)
         if (i < cnt) dst[i] = out[i];
@@ -99,87 +100,63 @@ __device__ __forceinline__ int i8_sum16(u32x4_t v, int acc) {
   return acc;
 }
 
-// Few rows: fragments straight from memory, the K range split over the KW
-// waves of a workgroup (and over gridDim.y workgroups through int32
-// partials). MT 16-row tiles, NT 16-column tiles.
-template <int MT, int NT, int KW, bool SILU, bool ZP, bool MOE>
-__global__ __launch_bounds__(64 * KW) void gemm_i8_rows_kernel(const I8Args p, int n_blocks) {
-  constexpr int TILES = MT * NT;
-  __shared__ i32x4_t red[KW * TILES * 64];
+// Up to 16 rows and few columns: fragments straight from memory, the K range
+// split over the KW waves of a workgroup that owns 16 columns of Y. Bound by
+// the weights' bytes: 16 KiB of loads in flight per CU at once and no barrier
+// in the loop (1 x 4096 x 4096: 5.5 us, 3.3 us of it loop = 5 TB/s; two
+// column tiles per workgroup 7.5 us, the 64 x 64 LDS tiles 9.9 us; from 8192 columns on those
+// are as fast, at 14336 faster: 12.2 against 17 us).
+template <int KW, bool SILU, bool ZP>
+__global__ __launch_bounds__(64 * KW) void gemm_i8_rows_kernel(const I8Args p) {
+  constexpr int NT = SILU ? 2 : 1;  // gate and up tile
+  __shared__ i32x4_t red[KW][NT][64];
   __shared__ int zred[KW][NT][16];
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int mb = blockIdx.x / n_blocks, nb = blockIdx.x % n_blocks;
-  int expert = 0;
-  if constexpr (MOE) {
-    if (mb * MT * 16 >= *p.num_padded) return;
-    expert = p.block_expert[mb];
-    if ((unsigned)expert >= (unsigned)p.num_experts) return;
-  }
-  const int8_t* ap[MT];
+  const int nb = blockIdx.x;
+  const int row = min(r, p.M - 1);
+  const int8_t* ap = p.A + (int64_t)row * p.lda;
   const int8_t* bp[NT];
-  int yrow[MT], arow[MT];  // yrow < 0: no row
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int row = mb * MT * 16 + mt * 16 + r;
-    if constexpr (MOE) {
-      const int id = p.sorted_ids[row];
-      const bool real = (unsigned)id < (unsigned)p.num_pairs;
-      yrow[mt] = real ? id : -1;
-      arow[mt] = real ? (p.a_per_pair ? id : id / p.top_k) : 0;
-    } else {
-      yrow[mt] = row < p.M ? row : -1;
-      arow[mt] = min(row, p.M - 1);
-    }
-    ap[mt] = p.A + (int64_t)arow[mt] * p.lda + 16 * c;
-  }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     int first, rows;
     i8_tile<SILU>(p, nb * NT + nt, first, rows);
-    bp[nt] = p.B + ((int64_t)expert * p.n + (rows > 0 ? first + min(r, rows - 1) : 0)) * p.ldb + 16 * c;
+    bp[nt] = p.B + (int64_t)(first + min(r, rows - 1)) * p.ldb;
   }
-  i32x4_t acc[MT][NT];
+  i32x4_t acc[NT];
   int zs[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     zs[nt] = 0;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt][nt] = i32x4_t{0, 0, 0, 0};
+    acc[nt] = i32x4_t{0, 0, 0, 0};
   }
   const int steps = (p.k + 63) / 64, full = p.k / 64;
-  const int parts = gridDim.y * KW, part = blockIdx.y * KW + wave;
-  const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
-#pragma unroll 1
+  const int s0 = steps * wave / KW, s1 = steps * (wave + 1) / KW;
   for (int s = s0; s < min(s1, full); ++s) {
-    u32x4_t a[MT], b[NT];
+    const int k0 = s * 64 + 16 * c;
+    u32x4_t b[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) b[nt] = *(const u32x4_t*)(bp[nt] + s * 64);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) a[mt] = *(const u32x4_t*)(ap[mt] + s * 64);
+    for (int nt = 0; nt < NT; ++nt) b[nt] = *(const u32x4_t*)(bp[nt] + k0);
+    const u32x4_t a = *(const u32x4_t*)(ap + k0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if constexpr (ZP) zs[nt] = i8_sum16(b[nt], zs[nt]);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) acc[mt][nt] = mfma_i8(b[nt], a[mt], acc[mt][nt]);
+      acc[nt] = mfma_i8(b[nt], a, acc[nt]);
     }
   }
-  if (s1 > full && s0 < s1) {  // the step that the row's end cuts
-    u32x4_t a[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) a[mt] = i8_load_tail(ap[mt] - 16 * c, full * 64 + 16 * c, p.k);
+  if (s1 > full) {  // the step that the row's end cuts
+    const int k0 = full * 64 + 16 * c;
+    const u32x4_t a = i8_load_tail(ap, k0, p.k);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const u32x4_t b = i8_load_tail(bp[nt] - 16 * c, full * 64 + 16 * c, p.k);
+      const u32x4_t b = i8_load_tail(bp[nt], k0, p.k);
       if constexpr (ZP) zs[nt] = i8_sum16(b, zs[nt]);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) acc[mt][nt] = mfma_i8(b, a[mt], acc[mt][nt]);
+      acc[nt] = mfma_i8(b, a, acc[nt]);
     }
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) red[(wave * TILES + mt * NT + nt) * 64 + lane] = acc[mt][nt];
+    red[wave][nt][lane] = acc[nt];
     if constexpr (ZP) {
       int z = zs[nt];
       z += __shfl_xor(z, 16);
@@ -188,82 +165,42 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_rows_kernel(const I8Args p, i
     }
   }
   __syncthreads();
-  constexpr int PER = SILU ? 2 : 1, UNITS = TILES / PER;
-  for (int un = wave; un < UNITS; un += KW) {
-    const int mt = un / (NT / PER), nt = un % (NT / PER) * PER;
-    i32x4_t v[2] = {};
-    int yr = -1, ar = 0;
+  if (wave != 0 || r >= p.M) return;
+  i32x4_t v[2] = {};
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      if (m == mt) {
-        yr = yrow[m];
-        ar = arow[m];
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int w = 0; w < KW; ++w) v[nt] += red[w][nt][lane];
+    if constexpr (ZP) {
+      const int za = p.a_zeros[r];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int z = 0;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) z += zred[w][nt][4 * c + i];
+        v[nt][i] -= za * z;
       }
-#pragma unroll
-    for (int h = 0; h < PER; ++h) {
-#pragma unroll
-      for (int w = 0; w < KW; ++w) v[h] += red[(w * TILES + mt * NT + nt + h) * 64 + lane];
-      if constexpr (ZP) {
-        const int za = p.a_zeros[ar];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          int z = 0;
-#pragma unroll
-          for (int w = 0; w < KW; ++w) z += zred[w][nt + h][4 * c + i];
-          v[h][i] -= za * z;
-        }
-      }
-    }
-    if (yr < 0) continue;
-    const int j0 = (nb * NT + nt) / PER * 16 + 4 * c;
-    if (gridDim.y > 1) {
-#pragma unroll
-      for (int h = 0; h < PER; ++h) {
-        int32_t* dst = p.partial + ((int64_t)blockIdx.y * p.M + yr) * p.n + h * p.cols + j0;
-        for (int i = 0; i < 4; ++i)
-          if (j0 + i < p.cols) dst[i] = v[h][i];
-      }
-    } else {
-      i8_finish<SILU>(p, v[0], v[1], yr, ar, expert, j0);
     }
   }
+  i8_finish<SILU>(p, v[0], v[1], r, r, nb * 16 + 4 * c);
 }
 
-// The partials of a split product, added and finished: one thread per row and
-// four columns of Y.
+// The partials of a split product (columns in the order of B's tiles), added
+// and finished: one thread per row and four columns of Y.
 template <bool SILU>
 __global__ __launch_bounds__(256) void gemm_i8_reduce_kernel(const I8Args p, int split) {
   const int64_t quads = (p.cols + 3) / 4;
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (t >= quads * p.M) return;
   const int row = (int)(t / quads), j0 = (int)(t % quads) * 4;
+  const int c = SILU ? j0 / 16 * 32 + j0 % 16 : j0;
   i32x4_t v[2] = {};
-  for (int s = 0; s < split; ++s)
-#pragma unroll
-    for (int h = 0; h < (SILU ? 2 : 1); ++h) {
-      const int32_t* src = p.partial + ((int64_t)s * p.M + row) * p.n + h * p.cols + j0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[h][i] += j0 + i < p.cols ? src[i] : 0;
-    }
-  i8_finish<SILU>(p, v[0], v[1], row, row, 0, j0);
-}
-
-template <int MT, int NT, int KW, bool MOE>
-hipError_t launch_rows(const I8Args& a, bool silu, int m_blocks, int split, hipStream_t s) {
-  const int tiles = (a.cols + 15) / 16 * (silu ? 2 : 1);
-  const int n_blocks = (tiles + NT - 1) / NT;
-  const int64_t blocks = (int64_t)m_blocks * n_blocks;
-  if (blocks * 64 * KW >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks, split);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(64 * KW), 0, s, a, n_blocks);
-    return hipGetLastError();
-  };
-  if (silu)
-    return a.a_zeros ? go(gemm_i8_rows_kernel<MT, NT, KW, true, true, MOE>)
-                     : go(gemm_i8_rows_kernel<MT, NT, KW, true, false, MOE>);
-  return a.a_zeros ? go(gemm_i8_rows_kernel<MT, NT, KW, false, true, MOE>)
-                   : go(gemm_i8_rows_kernel<MT, NT, KW, false, false, MOE>);
+  for (int s = 0; s < split; ++s) {
+    const int32_t* src = p.partial + ((int64_t)s * p.M + row) * p.vcols + c;
+    v[0] += *(const i32x4_t*)src;
+    if constexpr (SILU) v[1] += *(const i32x4_t*)(src + 16);
+  }
+  i8_finish<SILU>(p, v[0], v[1], row, row, j0);
 }
 
 // ------------------------------------------------------------- LDS tiles
@@ -383,7 +320,7 @@ __device__ __forceinline__ void i8_group(char* st, const char* next, const I8Src
                                          int load_g, int a_lane, int b_lane, const int (&at)[4], int half, int k,
                                          I8Frag<TM, TN>& f0, I8Frag<TM, TN>& f1, i32x16_t (&acc)[TM][TN],
                                          int (&zs)[TN]) {
-  constexpr int MF = TM * TN, H = MF / 2;
+  constexpr int MF = TM * TN, H = MF > 1 ? MF / 2 : 1;
   const int kk = g * 128 + half * 16;
   i8_frag_load(f1, st, a_lane, b_lane, at[1]);
   __builtin_amdgcn_sched_barrier(0);
@@ -411,25 +348,63 @@ __device__ __forceinline__ void i8_group(char* st, const char* next, const I8Src
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// The same for small wave tiles (at most 4 MFMAs a step): the fragments of
+// the whole next group are read under this group's MFMAs, where a read a step
+// ahead would wait out the LDS latency at every step.
+template <int LOADS, int NW, int TM, int TN, int LEFT, bool ZP, bool MASK, int TAG>
+__device__ __forceinline__ void i8_group_whole(char* st, const char* next, const I8Src<LOADS>& src, int wave, int g,
+                                               int load_g, int a_lane, int b_lane, const int (&at)[4], int half, int k,
+                                               I8Frag<TM, TN> (&f)[4], I8Frag<TM, TN> (&fn)[4],
+                                               i32x16_t (&acc)[TM][TN], int (&zs)[TN]) {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | (7 << 4) | (15 << 8) | ((LEFT >> 4) << 14));
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): f is here, the stage is free
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int s = 0; s < 4; ++s) i8_frag_load(fn[s], next, a_lane, b_lane, at[s]);
+  __builtin_amdgcn_sched_barrier(0);
+  i8_load_stage<0, LOADS, LOADS, NW, TAG>(st, src, wave, load_g);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    if constexpr (MASK) i8_frag_mask(f[s], g * 128 + (2 * s + half) * 16, k);
+    i8_frag_mma<0, TM * TN, TM, TN, ZP, TAG>(f[s], acc, zs);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 template <int WM, int WN, int TM, int TN, int NS, bool SILU, bool ZP, bool MOE>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args p, int m_blocks, int n_blocks) {
+__global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args p, int m_blocks, int n_blocks,
+                                                                     int m_run) {
   constexpr int NW = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN, BYTES = (BM + BN) * 128;
-  constexpr int LOADS = (BM + BN) / 8 / NW, TAG = ((WM * 8 + WN) * 8 + TM) * 64 + TN * 8 + SILU * 4 + ZP * 2 + MOE;
+  constexpr int LOADS = (BM + BN) / 8 / NW, TAG = ((WM * 8 + WN) * 8 + TM) * 512 + (TN * 8 + NS) * 8 + SILU * 4 + ZP * 2 + MOE;
   static_assert((BM + BN) / 8 % NW == 0, "every wave issues the same number of copies");
-  static_assert(NS == 2 || NS == 3, "two or three stages");
-  static_assert(NS * BYTES <= 160 * 1024, "stages exceed LDS");
+  static_assert(NS >= 2 && NS <= 8 && NS * BYTES <= 160 * 1024, "two to eight stages within LDS");
+  static_assert(LOADS * (NS - 1) < 64, "vmcnt holds the copies in flight");
+  // separate objects, so that the compiler can tell a copy into one stage
+  // from a read of another
   __shared__ __attribute__((aligned(1024))) char st0[BYTES];
   __shared__ __attribute__((aligned(1024))) char st1[BYTES];
-  __shared__ __attribute__((aligned(1024))) char st2[NS == 3 ? BYTES : 16];
-  char* const stage[3] = {st0, st1, st2};
+  __shared__ __attribute__((aligned(1024))) char st2[NS > 2 ? BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char st3[NS > 3 ? BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char st4[NS > 4 ? BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char st5[NS > 5 ? BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char st6[NS > 6 ? BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char st7[NS > 7 ? BYTES : 16];
+  char* const stage[8] = {st0, st1, st2, st3, st4, st5, st6, st7};
   const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
 
   int mb, nb;
   if constexpr (MOE) {
-    moe_tile_order(n_blocks, mb, nb);
-    if (mb >= m_blocks) return;  // the grid covers whole groups of 8 blocks
+    // an XCD takes runs of m_run blocks and walks them together, column block
+    // by column block: the blocks of one expert share its weights in that
+    // XCD's L2
+    const int x = blockIdx.x % 8, j = blockIdx.x / 8;
+    const int run = j / (m_run * n_blocks), at = j % (m_run * n_blocks);
+    mb = (run * 8 + x) * m_run + at % m_run;
+    nb = at / m_run;
+    if (mb >= m_blocks) return;  // the grid covers whole rounds of runs
   } else {
     // XCD x takes the x-th eighth of the tile order, which walks 4 x 8 blocks
     // of tiles (as in the 8-bit tiles over packed weights)
@@ -447,10 +422,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   }
   int expert = 0;
   if constexpr (MOE) {
-    if (mb * BM >= *p.num_padded) return;
+    if (mb * p.block_m >= *p.num_padded) return;
     expert = p.block_expert[mb];
     if ((unsigned)expert >= (unsigned)p.num_experts) return;
   }
+  // the pair behind a row of the tile, -1 for none (a 16-row block fills half
+  // of a 32-row tile)
+  auto pair_of = [&](int row) {
+    if (row >= p.block_m) return -1;
+    const int id = p.sorted_ids[mb * p.block_m + row];
+    return (unsigned)id < (unsigned)p.num_pairs ? id : -1;
+  };
   // 16-column tiles of B in the order the epilogue wants (gate and up tiles
   // alternate with SILU)
   const int vt0 = nb * (BN / 16);
@@ -462,10 +444,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
     const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3) ^ (i & 1)) * 16u;
     if (i < BM / 8) {
       if constexpr (MOE) {
-        const int id = p.sorted_ids[mb * BM + i * 8 + (lane >> 3)];
-        const int ar = (unsigned)id < (unsigned)p.num_pairs ? (p.a_per_pair ? id : id / p.top_k) : 0;
-        src.rsrc[q] = i8_rows_rsrc(p.A, 0, p.M, p.lda, k16);  // at most 4 GiB (checked by the host)
-        src.off[q] = (uint32_t)ar * (uint32_t)p.lda + chunk;
+        const int id = pair_of(i * 8 + (lane >> 3));
+        // A ends below kI8FarRow (checked by the host): rows that are not
+        // there read zeros behind it
+        src.rsrc[q] = i8_rows_rsrc(p.A, 0, p.M, p.lda, k16);
+        src.off[q] = id < 0 ? kI8FarRow : (uint32_t)(p.a_per_pair ? id : id / p.top_k) * (uint32_t)p.lda + chunk;
       } else {
         src.rsrc[q] = i8_rows_rsrc(p.A, mb * BM + i * 8, p.M, p.lda, k16);
         src.off[q] = (uint32_t)(lane >> 3) * (uint32_t)p.lda + chunk;
@@ -481,7 +464,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
       src.off[q] = (uint32_t)(lane >> 3) * (uint32_t)p.ldb + chunk;
     }
   }
-  const int groups = (p.k + 127) / 128;
+  // this workgroup's groups of K: [g0, groups)
+  const int all = (p.k + 127) / 128;
+  const int g0 = (int)((int64_t)all * blockIdx.y / gridDim.y), groups = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
   const int a_lane = (wm * TM * 32 + r) * 128, b_lane = (BM + wn * TN * 32 + r) * 128, sw = i8_swizzle(r);
   i32x16_t acc[TM][TN];
   int zs[TN];
@@ -498,28 +483,50 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   for (int q = 0; q < 4; ++q) at[q] = ((2 * q + half) ^ sw) * 16;
 #pragma unroll
   for (int q = 0; q < NS; ++q)
-    i8_load_stage<0, LOADS, LOADS, NW, TAG>(stage[q], src, wave, min(q, groups - 1));
+    i8_load_stage<0, LOADS, LOADS, NW, TAG>(stage[q], src, wave, min(g0 + q, groups - 1));
   constexpr int LEFT = LOADS * (NS - 1);
   __builtin_amdgcn_s_waitcnt((LEFT & 15) | (7 << 4) | (15 << 8) | ((LEFT >> 4) << 14));
   asm volatile("s_barrier" ::: "memory");
-  I8Frag<TM, TN> f0, f1;
-  i8_frag_load(f0, st0, a_lane, b_lane, at[0]);
-  const int full = p.k / 128;  // groups that need no mask
-  int g = 0;
-  for (; g + NS <= full; g += NS) {
+  const int full = min(p.k / 128, groups);  // groups that need no mask
+  int g = g0;
+  // full rounds of NS groups with constant stages, then the rest, the last
+  // group cut at k
+  if constexpr (TM * TN <= 4) {
+    static_assert(NS % 2 == 0, "the two fragment sets alternate with the stages");
+    I8Frag<TM, TN> f[2][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) i8_frag_load(f[0][q], st0, a_lane, b_lane, at[q]);
+    for (; g + NS <= full; g += NS) {
+#pragma unroll
+      for (int cur = 0; cur < NS; ++cur)
+        i8_group_whole<LOADS, NW, TM, TN, LOADS*(NS - 2), ZP, false, TAG + (1 << 20)>(
+            stage[cur], stage[(cur + 1) % NS], src, wave, g + cur, min(g + cur + NS, groups - 1), a_lane, b_lane, at,
+            half, p.k, f[cur % 2], f[(cur + 1) % 2], acc, zs);
+    }
+    // at most NS groups are left: all copied
 #pragma unroll
     for (int cur = 0; cur < NS; ++cur)
-      i8_group<LOADS, NW, TM, TN, LOADS*(NS - 2), ZP, false, TAG + (1 << 16)>(
-          stage[cur], stage[(cur + 1) % NS], src, wave, g + cur, min(g + cur + NS, groups - 1), a_lane, b_lane, at,
-          half, p.k, f0, f1, acc, zs);
-  }
-  // the remaining groups, the last one cut at k
+      if (g + cur < groups)
+        i8_group_whole<LOADS, NW, TM, TN, 0, ZP, true, TAG + (1 << 21)>(
+            stage[cur], stage[(cur + 1) % NS], src, wave, g + cur, groups - 1, a_lane, b_lane, at, half, p.k,
+            f[cur % 2], f[(cur + 1) % 2], acc, zs);
+  } else {
+    I8Frag<TM, TN> f0, f1;
+    i8_frag_load(f0, st0, a_lane, b_lane, at[0]);
+    for (; g + NS <= full; g += NS) {
 #pragma unroll
-  for (int cur = 0; cur < NS; ++cur)
-    if (g + cur < groups)
-      i8_group<LOADS, NW, TM, TN, 0, ZP, true, TAG + (1 << 17)>(
-          stage[cur], stage[(cur + 1) % NS], src, wave, g + cur, groups - 1, a_lane, b_lane, at, half, p.k, f0, f1,
-          acc, zs);
+      for (int cur = 0; cur < NS; ++cur)
+        i8_group<LOADS, NW, TM, TN, LOADS*(NS - 2), ZP, false, TAG + (1 << 20)>(
+            stage[cur], stage[(cur + 1) % NS], src, wave, g + cur, min(g + cur + NS, groups - 1), a_lane, b_lane, at,
+            half, p.k, f0, f1, acc, zs);
+    }
+#pragma unroll
+    for (int cur = 0; cur < NS; ++cur)
+      if (g + cur < groups)
+        i8_group<LOADS, NW, TM, TN, 0, ZP, true, TAG + (1 << 21)>(
+            stage[cur], stage[(cur + 1) % NS], src, wave, g + cur, groups - 1, a_lane, b_lane, at, half, p.k, f0, f1,
+            acc, zs);
+  }
   __builtin_amdgcn_s_waitcnt(0);  // the trailing copies have landed
   __syncthreads();
 
@@ -554,15 +561,13 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   const int wave_col = (vt0 * 16 + wn * TN * 32) / (SILU ? 2 : 1);
 #pragma unroll
   for (int m = 0; m < TM; ++m) {
-    const int grow = mb * BM + (wm * TM + m) * 32 + r;
-    int yr = grow, ar = min(grow, p.M - 1);
-    bool real = grow < p.M;
+    int yr = mb * BM + (wm * TM + m) * 32 + r, ar = min(yr, p.M - 1);  // yr < 0: no row
     if constexpr (MOE) {
-      yr = p.sorted_ids[grow];
-      real = (unsigned)yr < (unsigned)p.num_pairs;
-      ar = !real ? 0 : p.a_per_pair ? yr : yr / p.top_k;
+      yr = pair_of((wm * TM + m) * 32 + r);
+      ar = yr < 0 ? 0 : p.a_per_pair ? yr : yr / p.top_k;
+    } else if (yr >= p.M) {
+      yr = -1;
     }
-    yr = real ? yr : -1;
     const int za = ZP ? p.a_zeros[ar] : 0;
     const float sa = raw ? 1.f : p.a_scales[ar];
     auto sums = [&](int t, int q) {
@@ -593,7 +598,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
       return y;
     };
     // the strip's rows of `cols` columns of es bytes out, from column c0 on
-    auto flush = [&](int c0, int cols, int es) {
+    auto flush = [&](void* base, int64_t ld, int limit, int c0, int cols, int es) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       const int per = cols * es / 16;  // 16-byte pieces of a row
@@ -602,46 +607,61 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
         const int row = i / per, piece = i % per;
         const int y = __shfl(yr, row), j = c0 + piece * (16 / es);
         const u32x4_t v = *(const u32x4_t*)(strip + row * PITCH + piece * 16);
-        if (y < 0 || j >= p.cols) continue;
-        char* dst = (char*)p.Y + ((int64_t)y * p.ldy + j) * es;
-        if (p.y_vec && j + 16 / es <= p.cols) {
-          *(u32x4_t*)dst = v;
+        if (y < 0 || j >= limit) continue;
+        char* dst = (char*)base + ((int64_t)y * ld + j) * es;
+        if (j + 16 / es <= limit) {
+          *(u32x4_any_t*)dst = v;
         } else if (es == 4) {
-          for (int e = 0; e < 4 && j + e < p.cols; ++e) ((uint32_t*)dst)[e] = v[e];
+          for (int e = 0; e < 4 && j + e < limit; ++e) ((uint32_t*)dst)[e] = v[e];
         } else {
-          for (int e = 0; e < 8 && j + e < p.cols; ++e) ((uint16_t*)dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+          for (int e = 0; e < 8 && j + e < limit; ++e) ((uint16_t*)dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     };
-    if (p.otype == QDG_O_BF16) {
+    if (gridDim.y > 1) {  // dense: int32 partials, columns in the order of B's tiles
+#pragma unroll
+      for (int t = 0; t < TN; ++t) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *(i32x4_t*)(strip + r * PITCH + (q * 8 + half * 4) * 4) = sums(t, q);
+        flush(p.partial + (int64_t)blockIdx.y * p.M * p.vcols, p.vcols, p.vcols, vt0 * 16 + (wn * TN + t) * 32, 32,
+              4);
+      }
+    } else if (p.otype == QDG_O_BF16) {
 #pragma unroll
       for (int t = 0; t < TN; ++t)
 #pragma unroll
         for (int q = 0; q < TC / 8; ++q)
           *(u32x2_t*)(strip + r * PITCH + (t * TC + q * 8 + half * 4) * 2) = i8_bf16x4(out4(t, q));
-      flush(wave_col, TN * TC, 2);
+      flush(p.Y, p.ldy, p.cols, wave_col, TN * TC, 2);
     } else {
 #pragma unroll
       for (int t = 0; t < TN; ++t) {
 #pragma unroll
         for (int q = 0; q < TC / 8; ++q) *(f32x4_t*)(strip + r * PITCH + (q * 8 + half * 4) * 4) = out4(t, q);
-        flush(wave_col + t * TC, TC, 4);
+        flush(p.Y, p.ldy, p.cols, wave_col + t * TC, TC, 4);
       }
     }
   }
 }
 
 template <int WM, int WN, int TM, int TN, int NS, bool MOE>
-hipError_t launch_tile(const I8Args& a, bool silu, int m_blocks, hipStream_t s) {
+hipError_t launch_tile(const I8Args& a, bool silu, int m_blocks, int split, hipStream_t s) {
   constexpr int BN = 32 * TN * WN, THREADS = 64 * WM * WN;
-  const int tiles = (a.cols + 15) / 16 * (silu ? 2 : 1);
-  const int n_blocks = (tiles + BN / 16 - 1) / (BN / 16);
-  const int64_t blocks = (int64_t)(MOE ? moe_grid_blocks(m_blocks) : m_blocks) * n_blocks;
+  const int n_blocks = (a.vcols + BN - 1) / BN;
+  int64_t blocks = (int64_t)m_blocks * n_blocks;
+  int m_run = 1;
+  if (MOE) {
+    // runs of up to 8 blocks while every XCD still gets two (the blocks in
+    // use are at least num_pairs / block_m). T = 4096, 64-row blocks, gate+up:
+    // runs of 1 2.64 ms, 2 2.11, 4 2.08, 8 2.06, 16 2.05, 32 2.33
+    while (m_run < 8 && a.num_pairs / a.block_m >= 32 * m_run) m_run *= 2;
+    blocks = (int64_t)(m_blocks + 8 * m_run - 1) / (8 * m_run) * (8 * m_run) * n_blocks;
+  }
   if (blocks * THREADS >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(THREADS), 0, s, a, m_blocks, n_blocks);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks, split), dim3(THREADS), 0, s, a, m_blocks, n_blocks, m_run);
     return hipGetLastError();
   };
   if (silu)
@@ -651,22 +671,77 @@ hipError_t launch_tile(const I8Args& a, bool silu, int m_blocks, hipStream_t s) 
                    : go(gemm_i8_tile_kernel<WM, WN, TM, TN, NS, false, false, MOE>);
 }
 
+// ------------------------------------------------------------- dense choice
+// A dense product runs the rows kernel or one of four tiles, its K perhaps
+// split over workgroups. Measured on MI355X with the tiles filling the card
+// once: microseconds for one 128-byte group of K, and for a round's prologue
+// and epilogue. A product of R rounds of tiles over G groups takes about
+// R (G group + round) + 3 us (M = 256, n = 14336, k = 4096: 64 x 64 29 us, 128 x 64
+// 26, 128 x 128 22; M = n = k = 4096: 128 x 128 79, 256 x 256 66). A split adds a second kernel and the
+// partials' traffic (M = 64, n = 512, k = 16384: 25.4 us whole, 7.6 + 4.2 us in eight).
+enum I8Kernel { I8_ROWS, I8_64X64, I8_128X64, I8_128X128, I8_256X256 };
+struct I8Tile {
+  I8Kernel kernel;
+  int bm, bn;
+  float group, round;
+};
+constexpr I8Tile kI8Tiles[] = {{I8_64X64, 64, 64, 0.19f, 1.f},
+                               {I8_128X64, 128, 64, 0.33f, 1.5f},
+                               {I8_128X128, 128, 128, 0.53f, 2.f},
+                               {I8_256X256, 256, 256, 1.67f, 4.f}};
+constexpr int kCus = 256;
+
+I8Kernel choose_dense(int64_t M, int64_t vcols, int64_t k, bool silu, int* split) {
+  *split = 1;
+  if (M <= 16 && vcols < 8192) return I8_ROWS;
+  const int64_t groups = (k + 127) / 128;
+  I8Kernel best = I8_64X64;
+  float best_us = 0.f;
+  for (const I8Tile& t : kI8Tiles) {
+    const int64_t tiles = (M + t.bm - 1) / t.bm * ((vcols + t.bn - 1) / t.bn);
+    for (int s = 1; s <= 8; s *= 2) {
+      if (s > 1 && (tiles * s > kCus || groups < 8 * s)) break;
+      const float rounds = (float)((tiles * s + kCus - 1) / kCus);
+      float us = rounds * ((float)((groups + s - 1) / s) * t.group + t.round) + 3.f;
+      if (s > 1) us += 5.f + (float)(M * vcols * s) * 8e-6f / 4.f;  // written and read at about 4 TB/s
+      if (best_us == 0.f || us < best_us) {
+        best_us = us;
+        best = t.kernel;
+        *split = s;
+      }
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
-int gemm_i8_split(int64_t M, int64_t n, int64_t k, bool silu) { return 1; }
+int64_t gemm_i8_vcols(int64_t cols, bool silu) { return (cols + 15) / 16 * 16 * (silu ? 2 : 1); }
 
-hipError_t launch_gemm_i8(const I8Args& a, bool silu, int split, hipStream_t s) {
+int gemm_i8_split(int64_t M, int64_t vcols, int64_t k, bool silu) {
+  int split;
+  choose_dense(M, vcols, k, silu, &split);
+  return split;
+}
+
+hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s) {
+  int split;
   hipError_t e;
-  if (a.M <= 16)
-    e = launch_rows<1, 2, 8, false>(a, silu, 1, split, s);
-  else if (a.M <= 32)
-    e = launch_rows<2, 2, 8, false>(a, silu, 1, split, s);
-  else if (a.M <= 64)
-    e = launch_rows<4, 2, 8, false>(a, silu, 1, split, s);
-  else if (a.M <= 1024)
-    return launch_tile<2, 4, 2, 1, 3, false>(a, silu, (a.M + 127) / 128, s);
-  else
-    return launch_tile<2, 4, 4, 2, 2, false>(a, silu, (a.M + 255) / 256, s);
+  switch (choose_dense(a.M, a.vcols, a.k, silu, &split)) {
+    case I8_ROWS: {
+      const dim3 grid((unsigned)((a.cols + 15) / 16));
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(512), 0, s, a);
+        return hipGetLastError();
+      };
+      if (silu) return a.a_zeros ? go(gemm_i8_rows_kernel<8, true, true>) : go(gemm_i8_rows_kernel<8, true, false>);
+      return a.a_zeros ? go(gemm_i8_rows_kernel<8, false, true>) : go(gemm_i8_rows_kernel<8, false, false>);
+    }
+    case I8_64X64: e = launch_tile<2, 2, 1, 1, 4, false>(a, silu, (a.M + 63) / 64, split, s); break;
+    case I8_128X64: e = launch_tile<4, 2, 1, 1, 4, false>(a, silu, (a.M + 127) / 128, split, s); break;
+    case I8_128X128: e = launch_tile<2, 4, 2, 1, 4, false>(a, silu, (a.M + 127) / 128, split, s); break;
+    default: e = launch_tile<2, 4, 4, 2, 2, false>(a, silu, (a.M + 255) / 256, split, s); break;
+  }
   if (e != hipSuccess || split <= 1) return e;
   const int64_t threads = (int64_t)a.M * ((a.cols + 3) / 4);
   const dim3 grid((unsigned)((threads + 255) / 256));
@@ -677,16 +752,20 @@ hipError_t launch_gemm_i8(const I8Args& a, bool silu, int split, hipStream_t s) 
   return hipGetLastError();
 }
 
-hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int block_m, int m_blocks, hipStream_t s) {
-  // the tiles address A with 32 bits
-  const bool far = (int64_t)a.M * a.lda > (int64_t)0xFFFF0000;
-  if (far && block_m == 64) return launch_rows<4, 2, 8, true>(a, silu, m_blocks, 1, s);
-  if (far && block_m == 128) return launch_rows<8, 2, 4, true>(a, silu, m_blocks, 1, s);
-  switch (block_m) {
-    case 16: return launch_rows<1, 2, 8, true>(a, silu, m_blocks, 1, s);
-    case 32: return launch_rows<2, 2, 8, true>(a, silu, m_blocks, 1, s);
-    case 64: return launch_tile<2, 4, 1, 2, 3, true>(a, silu, m_blocks, s);
-    case 128: return launch_tile<2, 4, 2, 2, 3, true>(a, silu, m_blocks, s);
+// Expert blocks: the tile holds the block's rows. Two to four workgroups of
+// four waves share a CU, so that one's prologue and epilogue run under the others'
+// loops. Measured (E = 256, top-8; gate+up 4096 x 7168, down 7168 x 2048):
+//   16 rows  32 x 128 tiles half filled (fragments straight from memory: T = 64 down 640 us)
+//   32 rows  32 x 256: T = 512 down 646 us, 32 x 128 720, 32 x 64 759
+//   64 rows  64 x 256, four waves and two stages: T = 4096 gate+up 2.06 ms; eight waves and
+//            four stages (one workgroup a CU) 2.28, 64 x 128 2.35
+//   128 rows 128 x 128: T = 4096 gate+up 2.29 ms, 128 x 256 2.43
+hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int m_blocks, hipStream_t s) {
+  switch (a.block_m) {
+    case 16: return launch_tile<1, 4, 1, 1, 4, true>(a, silu, m_blocks, 1, s);
+    case 32: return launch_tile<1, 4, 1, 2, 2, true>(a, silu, m_blocks, 1, s);
+    case 64: return launch_tile<1, 4, 2, 2, 2, true>(a, silu, m_blocks, 1, s);
+    case 128: return launch_tile<2, 2, 2, 2, 2, true>(a, silu, m_blocks, 1, s);
     default: return hipErrorInvalidValue;
   }
 }

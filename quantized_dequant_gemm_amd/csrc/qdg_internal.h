@@ -174,17 +174,21 @@ struct I8Args {
   int M, n, k;             // M: rows of A (dense)
   int cols;                // columns of Y (n, or n / 2 with the SiLU*mul epilogue)
   int otype;
-  int y_vec;               // Y rows are 16-byte aligned
-  int32_t* partial;        // split K: int32 partials [split][M][n]
+  int vcols;               // columns of B's tiles in the kernels' order, whole tiles (gemm_i8_vcols)
+  int32_t* partial;        // split K: int32 partials [split][M][vcols]
   // grouped by expert (sorted_ids NULL: dense)
   const int32_t* sorted_ids;
   const int32_t* block_expert;
   const int32_t* num_padded;
-  int num_experts, num_pairs, top_k, a_per_pair;
+  int num_experts, num_pairs, top_k, a_per_pair, block_m;
 };
-int gemm_i8_split(int64_t M, int64_t n, int64_t k, bool silu);
-hipError_t launch_gemm_i8(const I8Args& a, bool silu, int split, hipStream_t s);
-hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int block_m, int m_blocks, hipStream_t s);
+// A of a grouped product ends below this offset (the tiles address its rows
+// with 32 bits, and rows that are not there behind it)
+constexpr uint32_t kI8FarRow = 0xF0000000u;
+int64_t gemm_i8_vcols(int64_t cols, bool silu);
+int gemm_i8_split(int64_t M, int64_t vcols, int64_t k, bool silu);
+hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s);
+hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int m_blocks, hipStream_t s);
 
 #endif
 

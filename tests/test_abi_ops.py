@@ -114,6 +114,7 @@ def test_moe_refusals():
     assert _moe(T=(1 << 19) + 1) == uns
     assert _moe(sid=None) == inv and _moe(blk=None) == inv and _moe(npad=None) == inv
     assert _moe(sid=P + 2) == mis and _moe(npad=P + 1) == mis
+    assert _moe(T=1 << 17, top_k=8, lda=1 << 15) == uns  # 4 GiB of token rows
     assert _moe(A=None) == inv and _moe(Y=None) == inv and _moe(B=P + 4) == mis
 
 
