@@ -197,66 +197,197 @@ hipError_t launch_act_i8_planes(const int8_t* qa, int64_t rows, int64_t K, uint8
 
 namespace {
 
-// Asymmetric int8 per token (qdg_quantize_act_zp): one workgroup per row.
-// The range [lo, hi] of the row's finite values and 0 maps onto the 256
-// codes; scale, zero point and codes are decided in binary64 from the
-// binary32 scale.
+// Asymmetric int8 per token (qdg_quantize_act_zp). The range [lo, hi] of the
+// row's finite values and 0 maps onto the 256 codes; scale, zero point and
+// codes are decided in binary64 from the binary32 scale. Bound by its bytes,
+// 2 k read and k written a row: TPR threads hold a row in registers (CH
+// chunks of 16 values each) between the range and the encoding, so it is read once.
+// M = 4096, k = 14336: 40.6 us (4.3 TB/s); 53.7 us with a second read and binary64
+// throughout.
+//
+// Range: a bf16 word as int16 orders the values from 0 up, as uint16 the
+// negative ones by magnitude above all others, so hi and lo are packed
+// 16-bit maxima; an infinity or a NaN shows as a maximum past the largest
+// finite word, and only then the row's values are checked one by one.
+// Encoding: y = fma(x, inv32, 1.5 * 2^23) carries rne(x * inv32) in its low
+// bits. inv32 is off by 2^-24 of itself and |x * inv| <= 256, so the code is the
+// binary64 one unless x * inv32 is within 2^-16 of the middle between two
+// integers (kDoubt = 2^-15 is used); a chunk with such a value (or NaN) is encoded again
+// in binary64: one chunk of 64 lanes in 16.
+constexpr float kDoubt = 0.5f - 0x1p-15f;
+
+__device__ __forceinline__ uint32_t pk_max_i16(uint32_t a, uint32_t b) {
+  typedef __attribute__((ext_vector_type(2))) short i16x2_t;
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(i16x2_t, a), __builtin_bit_cast(i16x2_t, b)));
+}
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2_t;
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
+}
+
+// 16 values of a row from i on (dword d holds values 2 d and 2 d + 1), 0
+// behind its end. The 16 bytes at i and at i + 8 are read only where they
+// start inside the row.
+__device__ __forceinline__ void load16(const uint16_t* x, int64_t i, int64_t k, uint32_t (&v)[8]) {
+  const u32x4_t z = {0, 0, 0, 0};
+  const u32x4_t a = i < k ? *(const u32x4_t*)(x + i) : z, b = i + 8 < k ? *(const u32x4_t*)(x + i + 8) : z;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    v[d] = a[d];
+    v[4 + d] = b[d];
+  }
+  if (i + 16 > k) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) v[d] &= i + 2 * d + 1 < k ? ~0u : i + 2 * d < k ? 0xFFFFu : 0u;
+  }
+}
+
+struct ZpRow {
+  float scale, inv32;
+  double inv, zero;
+};
+
+__device__ __forceinline__ ZpRow zp_row(float lo, float hi) {
+  const bool any = hi > lo;
+  ZpRow z;
+  z.scale = any ? fmaxf((float)(((double)hi - (double)lo) / 255.0), 0x1p-126f) : 1.0f;
+  z.inv = 1.0 / (double)z.scale;
+  z.inv32 = (float)z.inv;
+  z.zero = any ? fmin(fmax(rint(-128.0 - (double)lo * z.inv), -128.0), 127.0) : 0.0;
+  return z;
+}
+
+// The codes of 16 values into q + i.
+__device__ __forceinline__ void encode16(const uint32_t (&v)[8], const ZpRow& z, int8_t* q, int64_t i, int64_t k) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+  const int shift = (int)z.zero - 0x4B400000;
+  uint32_t out[4];
+  bool doubt = false;
+  int c[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float f = __builtin_bit_cast(float, j & 1 ? v[j >> 1] & 0xFFFF0000u : v[j >> 1] << 16);
+    const float y = __builtin_fmaf(f, z.inv32, kMagic);
+    doubt |= !(fabsf(__builtin_fmaf(f, z.inv32, kMagic - y)) < kDoubt);
+    c[j] = min(max(__builtin_bit_cast(int, y) + shift, -128), 127);
+  }
+  if (doubt) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float f = __builtin_bit_cast(float, j & 1 ? v[j >> 1] & 0xFFFF0000u : v[j >> 1] << 16);
+      const double d = f == f ? rint((double)f * z.inv) : 0.0;
+      c[j] = (int)fmin(fmax(d + z.zero, -128.0), 127.0);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+    out[d] = ((uint32_t)c[4 * d] & 0xFFu) | ((uint32_t)c[4 * d + 1] & 0xFFu) << 8 |
+             ((uint32_t)c[4 * d + 2] & 0xFFu) << 16 | (uint32_t)c[4 * d + 3] << 24;
+  if (i + 16 <= k) {
+    *(u32x4_t*)(q + i) = u32x4_t{out[0], out[1], out[2], out[3]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (i + j < k) q[i + j] = (int8_t)(out[j >> 2] >> (8 * (j & 3)));
+  }
+}
+
+// The largest of both over the TPR threads of a row.
+template <int TPR>
+__device__ __forceinline__ void row_max2(uint32_t& a, uint32_t& b, uint32_t (&buf)[2][4]) {
+  for (int m = 32; m > 0; m >>= 1) {
+    a = max(a, (uint32_t)__shfl_xor((int)a, m));
+    b = max(b, (uint32_t)__shfl_xor((int)b, m));
+  }
+  if constexpr (TPR == 256) {
+    __syncthreads();  // a row before has read the buffer
+    if ((threadIdx.x & 63) == 0) {
+      buf[0][threadIdx.x >> 6] = a;
+      buf[1][threadIdx.x >> 6] = b;
+    }
+    __syncthreads();
+    a = max(max(buf[0][0], buf[0][1]), max(buf[0][2], buf[0][3]));
+    b = max(max(buf[1][0], buf[1][1]), max(buf[1][2], buf[1][3]));
+  }
+}
+
+// CH > 0: a row of at most 16 TPR CH values in registers; CH = 0: any length,
+// read twice.
+template <int TPR, int CH>
 __global__ __launch_bounds__(256) void act_int8_zp_kernel(const uint16_t* __restrict__ a, int64_t lda, int64_t M,
                                                           int64_t k, int8_t* __restrict__ q, int64_t ldq,
                                                           float* __restrict__ scales, int32_t* __restrict__ zeros) {
-  __shared__ float wlo[4], whi[4];
-  for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
+  __shared__ uint32_t buf[2][4];
+  constexpr int RPB = 256 / TPR;
+  const int t = threadIdx.x % TPR;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < M; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t row = r0 + threadIdx.x / TPR;
+    if (TPR < 256 && row >= M) break;  // whole waves: no barrier below
     const uint16_t* x = a + row * lda;
-    float lo = 0.f, hi = 0.f;
-    for (int64_t i = threadIdx.x * 8; i < k; i += 256 * 8) {
-      // the 16 bytes start inside the row; values behind its end do not count
-      const u32x4_t v = *(const u32x4_t*)(x + i);
+    uint32_t v[CH ? CH : 1][8];
+    const int chunks = CH ? CH : (int)((k + 16 * TPR - 1) / (16 * TPR));
+    uint32_t pos = 0, neg = 0;  // packed maxima
+    auto chunk_max = [&](const uint32_t(&w)[8]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float f = bf16_to_f32(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xFFFFu);
-        if (i + j < k && fabsf(f) < __builtin_inff()) {
-          lo = fminf(lo, f);
-          hi = fmaxf(hi, f);
+      for (int d = 0; d < 8; ++d) {
+        pos = pk_max_i16(pos, w[d]);
+        neg = pk_max_u16(neg, w[d]);
+      }
+    };
+    if constexpr (CH > 0) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) load16(x, (int64_t)(c * TPR + t) * 16, k, v[c]);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) chunk_max(v[c]);
+    } else {
+      for (int c = 0; c < chunks; ++c) {
+        load16(x, ((int64_t)c * TPR + t) * 16, k, v[0]);
+        chunk_max(v[0]);
+      }
+    }
+    uint32_t hw = max(pos & 0xFFFFu, pos >> 16), lw = max(neg & 0xFFFFu, neg >> 16);
+    row_max2<TPR>(hw, lw, buf);
+    if (hw >= 0x7F80u || lw >= 0xFF80u) {  // an infinity or a NaN: they do not count
+      hw = lw = 0;
+      auto finite_max = [&](const uint32_t(&w)[8]) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t h = j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu;
+          if ((h & 0x7FFFu) < 0x7F80u) {
+            if (h < 0x8000u) hw = max(hw, h);
+            lw = max(lw, h);
+          }
+        }
+      };
+      if constexpr (CH > 0) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) finite_max(v[c]);
+      } else {
+        for (int c = 0; c < chunks; ++c) {
+          load16(x, ((int64_t)c * TPR + t) * 16, k, v[0]);
+          finite_max(v[0]);
         }
       }
+      row_max2<TPR>(hw, lw, buf);
     }
-    for (int off = 32; off > 0; off >>= 1) {
-      lo = fminf(lo, __shfl_xor(lo, off));
-      hi = fmaxf(hi, __shfl_xor(hi, off));
+    const ZpRow z = zp_row(lw >= 0x8000u ? bf16_to_f32(lw) : 0.f, bf16_to_f32(hw));
+    if (t == 0) {
+      scales[row] = z.scale;
+      zeros[row] = (int32_t)z.zero;
     }
-    if ((threadIdx.x & 63) == 0) {
-      wlo[threadIdx.x >> 6] = lo;
-      whi[threadIdx.x >> 6] = hi;
-    }
-    __syncthreads();
-    lo = fminf(fminf(wlo[0], wlo[1]), fminf(wlo[2], wlo[3]));
-    hi = fmaxf(fmaxf(whi[0], whi[1]), fmaxf(whi[2], whi[3]));
-    const bool any = hi > lo;
-    const float scale = any ? fmaxf((float)(((double)hi - (double)lo) / 255.0), 0x1p-126f) : 1.0f;
-    const double inv = 1.0 / (double)scale;
-    const double zero = any ? fmin(fmax(rint(-128.0 - (double)lo * inv), -128.0), 127.0) : 0.0;
-    if (threadIdx.x == 0) {
-      scales[row] = scale;
-      zeros[row] = (int32_t)zero;
-    }
-    for (int64_t i = threadIdx.x * 8; i < k; i += 256 * 8) {
-      const u32x4_t v = *(const u32x4_t*)(x + i);
-      uint32_t out[2] = {0, 0};
+    int8_t* y = q + row * ldq;
+    if constexpr (CH > 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float f = bf16_to_f32(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xFFFFu);
-        const double d = f == f ? rint((double)f * inv) : 0.0;
-        const int code = (int)fmin(fmax(d + zero, -128.0), 127.0);
-        out[j >> 2] |= ((uint32_t)code & 0xFFu) << (8 * (j & 3));
-      }
-      int8_t* dst = q + row * ldq + i;
-      if (i + 8 <= k) {
-        *(u32x2_t*)dst = u32x2_t{out[0], out[1]};
-      } else {
-        for (int j = 0; i + j < k; ++j) dst[j] = (int8_t)(out[j >> 2] >> (8 * (j & 3)));
+      for (int c = 0; c < CH; ++c)
+        if ((int64_t)(c * TPR + t) * 16 < k) encode16(v[c], z, y, (int64_t)(c * TPR + t) * 16, k);
+    } else {
+      for (int c = 0; c < chunks; ++c) {
+        const int64_t i = ((int64_t)c * TPR + t) * 16;
+        if (i >= k) break;
+        load16(x, i, k, v[0]);
+        encode16(v[0], z, y, i, k);
       }
     }
-    __syncthreads();  // the row's minima are read before the next row's are written
   }
 }
 
@@ -264,10 +395,17 @@ __global__ __launch_bounds__(256) void act_int8_zp_kernel(const uint16_t* __rest
 
 hipError_t launch_quantize_act_zp(const void* a, int64_t lda, int64_t M, int64_t k, int8_t* qa, int64_t ldq,
                                   float* scales, int32_t* zeros, hipStream_t s) {
-  const unsigned grid = (unsigned)(M < (1 << 20) ? M : 1 << 20);
-  hipLaunchKernelGGL(act_int8_zp_kernel, dim3(grid), dim3(256), 0, s, (const uint16_t*)a, lda, M, k, qa, ldq, scales,
-                     zeros);
-  return hipGetLastError();
+  auto go = [&](auto kernel, int64_t rows_per_block) {
+    const int64_t blocks = (M + rows_per_block - 1) / rows_per_block;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256), 0, s,
+                       (const uint16_t*)a, lda, M, k, qa, ldq, scales, zeros);
+    return hipGetLastError();
+  };
+  if (k <= 1024) return go(act_int8_zp_kernel<64, 1>, 4);
+  if (k <= 4096) return go(act_int8_zp_kernel<256, 1>, 1);
+  if (k <= 8192) return go(act_int8_zp_kernel<256, 2>, 1);
+  if (k <= 16384) return go(act_int8_zp_kernel<256, 4>, 1);
+  return go(act_int8_zp_kernel<256, 0>, 1);
 }
 
 hipError_t launch_quantize_act(int atype, const void* a, int64_t M, int64_t K, void* qa, float* scales,
