@@ -32,6 +32,7 @@
 // last place, 2^-23) of the argument's upper part, times 1 + its lower part;
 // sums and quotients in binary64, so a weight is off by 2^-22 + 2^-24.
 #include <algorithm>
+#include <type_traits>
 
 #include "qdg_device.h"
 #include "qdg_internal.h"
@@ -296,7 +297,7 @@ __device__ __forceinline__ double rcp64(double v) {
   return __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
 }
 
-template <int EPL>
+template <int EPL, bool SIGMOID, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
     const qdg_route_config c, const void* __restrict__ logits, int64_t ld, const float* __restrict__ bias, int64_t T,
     bool vec, int group_shift, uint32_t index_mask, int32_t* __restrict__ ids, float* __restrict__ weights,
@@ -304,190 +305,191 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
   __shared__ float keybuf[kWavesPerBlock][EPL * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int E = c.num_experts, G = c.num_groups, per = E / G, e0 = lane * EPL;
+  const int E = c.num_experts, G = GROUPS ? c.num_groups : 1, per = E / G, e0 = lane * EPL;
   float b[EPL];
   bool bad_bias = false;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    b[j] = bias && e0 + j < E ? bias[e0 + j] : 0.f;
+    b[j] = BIAS && e0 + j < E ? bias[e0 + j] : 0.f;
     bad_bias |= b[j] != b[j];
   }
-  for (int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + wave; t < T; t += (int64_t)gridDim.x * kWavesPerBlock) {
-    Row row{(const char*)logits + t * ld * (c.ltype == QDG_L_F32 ? 4 : 2), bias, c.ltype, c.score, E, 0.f, 1.0};
-    float x[EPL];  // logits, -inf where masked by the logit
-    load_row<EPL>(row.logits, c.ltype, vec, e0, E, -kInf, x);
-    bool bad = bad_bias;
+  // one token a wave: in a loop over tokens the constants of the rare binary64
+  // paths would be kept in registers for all of it
+  const int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + wave;
+  if (t >= T) return;  // whole waves; no barrier below
+  Row row{(const char*)logits + t * ld * (c.ltype == QDG_L_F32 ? 4 : 2), bias, c.ltype, c.score, E, 0.f, 1.0};
+  float x[EPL];  // logits, -inf where masked by the logit
+  load_row<EPL>(row.logits, c.ltype, vec, e0, E, -kInf, x);
+  bool bad = bad_bias;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      bad |= x[j] != x[j] || x[j] == kInf;
-      x[j] = x[j] != x[j] ? -kInf : fminf(x[j], kMax);
-    }
-    if (status && bad) atomicOr(status, (uint32_t)QDG_FLAG_BAD_LOGIT);
-    if (c.score == QDG_SCORE_SOFTMAX) {
-      float top = x[0];
+  for (int j = 0; j < EPL; ++j) {
+    bad |= x[j] != x[j] || x[j] == kInf;
+    x[j] = x[j] != x[j] ? -kInf : fminf(x[j], kMax);
+  }
+  if (status && bad) atomicOr(status, (uint32_t)QDG_FLAG_BAD_LOGIT);
+  if constexpr (!SIGMOID) {
+    float top = x[0];
 #pragma unroll
-      for (int j = 1; j < EPL; ++j) top = fmaxf(top, x[j]);
-      row.top = of_order(wave_max(order_of(top)));
-    }
+    for (int j = 1; j < EPL; ++j) top = fmaxf(top, x[j]);
+    row.top = of_order(wave_max(order_of(top)));
+  }
 
-    float key[EPL];  // s + bias; -inf where masked
-    if (bias || G > 1) {
-      float inv = 1.f;
-      if (c.score == QDG_SCORE_SOFTMAX) {
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          key[j] = x[j] == -kInf ? 0.f : __expf(x[j] - row.top);
-          sum += key[j];
-        }
-        for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
-        inv = __builtin_amdgcn_rcpf(sum);
-      }
+  float key[EPL];  // s + bias; -inf where masked
+  if constexpr (BIAS || GROUPS) {
+    float inv = 1.f;
+    if constexpr (!SIGMOID) {
+      float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        const float s = c.score == QDG_SCORE_SOFTMAX ? key[j] * inv : __builtin_amdgcn_rcpf(1.0f + __expf(-x[j]));
-        key[j] = x[j] == -kInf || !(b[j] > -kInf) ? -kInf : s + b[j];
+        key[j] = x[j] == -kInf ? 0.f : __expf(x[j] - row.top);
+        sum += key[j];
       }
+      for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+      inv = __builtin_amdgcn_rcpf(sum);
     }
-
-    uint64_t stay = ~0ull;
-    if (G > 1) {
-      float m1 = -kInf, m2 = -kInf;  // lane of group g: its two largest keys
-      int owner = lane;              // the lane that holds group g = lane's
-      if (group_shift >= 0) {
-        // a group is 2^group_shift whole lanes
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) top2_add(m1, m2, e0 + j < E ? key[j] : -kInf);
-        for (int m = 1; m < 1 << group_shift; m <<= 1) {
-          const float o1 = __shfl_xor(m1, m), o2 = __shfl_xor(m2, m);
-          m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
-          m1 = fmaxf(m1, o1);
-        }
-        owner = lane << group_shift;
-      } else {
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) keybuf[wave][e0 + j] = key[j];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (lane < G)
-          for (int i = 0; i < per; ++i) top2_add(m1, m2, keybuf[wave][lane * per + i]);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-      }
-      float v = c.group_score == QDG_GROUP_MAX || m2 == -kInf ? m1 : m1 + m2;
-      // two keys' errors and the roundings of keys and sum
-      const float err = fabsf(v) < kInf ? 2.f * kScoreErr + (fabsf(m1) + (m2 == -kInf ? 0.f : fabsf(m2))) * 0x1p-22f : 0.f;
-      v = __shfl(v, owner & 63);
-      const float dv = __shfl(err, owner & 63);
-      const float vl = v - dv, vu = v + dv;
-      int maybe = 0;  // groups that may be ahead of this lane's
-      for (int g = 0; g < G; ++g) {
-        const float ou = readlane_f32(vu, g);
-        const bool tie = ou == -kInf && vu == -kInf;  // all masked, both: the index decides
-        maybe += g != lane && (tie ? g < lane : ou >= vl);
-      }
-      const bool in = lane < G && maybe < c.topk_groups;
-      stay = __ballot(in);
-      if (__popcll(stay) != c.topk_groups) stay = groups64(row, c, lane);
-    }
-
-    // the ordered keys
-    const bool lane_stays = group_shift < 0 || (stay >> (lane >> group_shift)) & 1;
-    uint32_t o[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      const int e = e0 + j;
-      const bool stays = group_shift < 0 && G > 1 ? e < E && (stay >> (e / per)) & 1 : lane_stays;
-      // -0 and 0 are one key
-      o[j] = e < E && stays ? (order_of((bias ? key[j] : x[j]) + 0.f) & ~index_mask) | (index_mask - (uint32_t)e) : 0u;
+      const float s = !SIGMOID ? key[j] * inv : __builtin_amdgcn_rcpf(1.0f + __expf(-x[j]));
+      key[j] = x[j] == -kInf || !(b[j] > -kInf) ? -kInf : s + b[j];
     }
-    if constexpr (EPL == 2) sort2(o[0], o[1]);
-    if constexpr (EPL == 4) {
-      sort2(o[0], o[1]);
-      sort2(o[2], o[3]);
-      sort2(o[0], o[2]);
-      sort2(o[1], o[3]);
-      sort2(o[1], o[2]);
-    }
-    // rounds 0 .. top_k: lane r keeps the r-th largest
-    uint32_t mine = 0;
-    for (int r = 0; r <= c.top_k; ++r) {
-      const uint32_t m = take_largest<EPL>(o);
-      mine = lane == r ? m : mine;
-    }
-    if (bias || c.ltype == QDG_L_F32) {
-      // does each gap to the next decide?
-      const uint32_t next = (uint32_t)__shfl_down((int)mine, 1);
-      const bool checked = lane < c.top_k && next != 0 && (mine & ~index_mask) != (order_of(-kInf) & ~index_mask);
-      const bool sure = bias ? key_low(mine, index_mask) > key_high(next, index_mask)
-                             : (mine ^ next) > index_mask;  // exact but for the cut bits
-      if (__ballot(checked && !sure)) {
-        // kMore candidates more, ranked by binary64 keys, one lane each
-        uint32_t last = 0;
-        for (int r = c.top_k + 1; r < c.top_k + kMore; ++r) {
-          last = take_largest<EPL>(o);
-          mine = lane == r ? last : mine;
-        }
-        if (c.score == QDG_SCORE_SOFTMAX && bias) row.set_sum(lane);
-        int cand = (int)(index_mask - (mine & index_mask));
-        double k = kNegInf64;
-        if (mine != 0) k = bias ? row.key64(cand) : (double)row.logit(cand);
-        else cand = 1 << 30;
-        int rank = 0;
-        for (int i = 0; i < c.top_k + kMore; ++i) {
-          const double ok = readlane_f64(k, i);
-          const int oc = __builtin_amdgcn_readlane(cand, i);
-          rank += ok > k || (ok == k && oc < cand);
-        }
-        // what was not taken is at most `last`; masked experts follow the index
-        const uint64_t kth = __ballot(lane < c.top_k + kMore && rank == c.top_k - 1);
-        const double kth_key = readlane_f64(k, __builtin_ctzll(kth));
-        const double rest = bias ? (double)key_high(last, index_mask) : (double)of_order(last | index_mask);
-        const bool whole = last == 0 || (last & ~index_mask) == (order_of(-kInf) & ~index_mask);
-        int id = 0;
-        if (whole || kth_key > rest) {
-          for (int i = 0; i < c.top_k + kMore; ++i) {
-            const int to = __builtin_amdgcn_readlane(rank, i), oc = __builtin_amdgcn_readlane(cand, i);
-            if (lane == to) id = oc;
-          }
-        } else {
-          id = route64(row, c, stay, lane);
-        }
-        mine = index_mask - (uint32_t)id;
-      }
-    }
-    const int id = (int)(index_mask - (mine & index_mask));
+  }
 
-    // the weights
-    float my_x = -kInf;
-    if (lane < c.top_k) {
-      my_x = row.logit(id);
-      if (bias && !(bias[id] > -kInf)) my_x = -kInf;  // masked: weight 0
-    }
-    double w = 0.0;
-    const bool sigmoid = c.score == QDG_SCORE_SIGMOID;
-    // renormalised softmax weights need no more than the chosen experts' ratios
-    const float ref = sigmoid ? 0.f : c.renormalize ? of_order(wave_max(order_of(my_x))) : row.top;
-    const float arg = sigmoid ? my_x : my_x - ref;
-    if (__ballot(my_x != -kInf && arg < -80.f)) {  // near or past the end of binary32
-      if (my_x != -kInf) w = sigmoid ? sigmoid64((double)my_x) : exp((double)my_x - (double)ref);
-    } else if (my_x != -kInf) {
-      w = sigmoid ? rcp64(1.0 + (double)expf(-my_x)) : exp_diff(my_x, ref);
-    }
-    if (c.renormalize) {
-      row.sum64 = w;
-      for (int m = 1; m < c.top_k; m <<= 1) row.sum64 += __shfl_xor(row.sum64, m);
-    } else if (!sigmoid) {
-      double sum = 0.0;
+  uint64_t stay = ~0ull;
+  if constexpr (GROUPS) {
+    float m1 = -kInf, m2 = -kInf;  // lane of group g: its two largest keys
+    int owner = lane;              // the lane that holds group g = lane's
+    if (group_shift >= 0) {
+      // a group is 2^group_shift whole lanes
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) sum += x[j] == -kInf ? 0.0 : exp_diff(x[j], row.top);
-      row.sum64 = wave_sum(sum);
+      for (int j = 0; j < EPL; ++j) top2_add(m1, m2, e0 + j < E ? key[j] : -kInf);
+      for (int m = 1; m < 1 << group_shift; m <<= 1) {
+        const float o1 = __shfl_xor(m1, m), o2 = __shfl_xor(m2, m);
+        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+        m1 = fmaxf(m1, o1);
+      }
+      owner = lane << group_shift;
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) keybuf[wave][e0 + j] = key[j];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (lane < G)
+        for (int i = 0; i < per; ++i) top2_add(m1, m2, keybuf[wave][lane * per + i]);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-    if (c.renormalize || !sigmoid) w = row.sum64 > 0.0 ? w * rcp64(row.sum64) : 0.0;
-    if (lane < c.top_k) {
-      ids[t * c.top_k + lane] = id;
-      weights[t * c.top_k + lane] = (float)(w * (double)c.scale);
+    float v = c.group_score == QDG_GROUP_MAX || m2 == -kInf ? m1 : m1 + m2;
+    // two keys' errors and the roundings of keys and sum
+    const float err = fabsf(v) < kInf ? 2.f * kScoreErr + (fabsf(m1) + (m2 == -kInf ? 0.f : fabsf(m2))) * 0x1p-22f : 0.f;
+    v = __shfl(v, owner & 63);
+    const float dv = __shfl(err, owner & 63);
+    const float vl = v - dv, vu = v + dv;
+    int maybe = 0;  // groups that may be ahead of this lane's
+    for (int g = 0; g < G; ++g) {
+      const float ou = readlane_f32(vu, g);
+      const bool tie = ou == -kInf && vu == -kInf;  // all masked, both: the index decides
+      maybe += g != lane && (tie ? g < lane : ou >= vl);
     }
+    const bool in = lane < G && maybe < c.topk_groups;
+    stay = __ballot(in);
+    if (__popcll(stay) != c.topk_groups) stay = groups64(row, c, lane);
+  }
+
+  // the ordered keys
+  const bool lane_stays = group_shift < 0 || (stay >> (lane >> group_shift)) & 1;
+  uint32_t o[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = e0 + j;
+    const bool stays = GROUPS && group_shift < 0 ? e < E && (stay >> (e / per)) & 1 : lane_stays;
+    // -0 and 0 are one key
+    o[j] = e < E && stays ? (order_of((BIAS ? key[j] : x[j]) + 0.f) & ~index_mask) | (index_mask - (uint32_t)e) : 0u;
+  }
+  if constexpr (EPL == 2) sort2(o[0], o[1]);
+  if constexpr (EPL == 4) {
+    sort2(o[0], o[1]);
+    sort2(o[2], o[3]);
+    sort2(o[0], o[2]);
+    sort2(o[1], o[3]);
+    sort2(o[1], o[2]);
+  }
+  // rounds 0 .. top_k: lane r keeps the r-th largest
+  uint32_t mine = 0;
+  for (int r = 0; r <= c.top_k; ++r) {
+    const uint32_t m = take_largest<EPL>(o);
+    mine = lane == r ? m : mine;
+  }
+  if (BIAS || c.ltype == QDG_L_F32) {
+    // does each gap to the next decide?
+    const uint32_t next = (uint32_t)__shfl_down((int)mine, 1);
+    const bool checked = lane < c.top_k && next != 0 && (mine & ~index_mask) != (order_of(-kInf) & ~index_mask);
+    const bool sure = BIAS ? key_low(mine, index_mask) > key_high(next, index_mask)
+                           : (mine ^ next) > index_mask;  // exact but for the cut bits
+    if (__ballot(checked && !sure)) {
+      // kMore candidates more, ranked by binary64 keys, one lane each
+      uint32_t last = 0;
+      for (int r = c.top_k + 1; r < c.top_k + kMore; ++r) {
+        last = take_largest<EPL>(o);
+        mine = lane == r ? last : mine;
+      }
+      if (!SIGMOID && BIAS) row.set_sum(lane);
+      int cand = (int)(index_mask - (mine & index_mask));
+      double k = kNegInf64;
+      if (mine != 0) k = BIAS ? row.key64(cand) : (double)row.logit(cand);
+      else cand = 1 << 30;
+      int rank = 0;
+      for (int i = 0; i < c.top_k + kMore; ++i) {
+        const double ok = readlane_f64(k, i);
+        const int oc = __builtin_amdgcn_readlane(cand, i);
+        rank += ok > k || (ok == k && oc < cand);
+      }
+      // what was not taken is at most `last`; masked experts follow the index
+      const uint64_t kth = __ballot(lane < c.top_k + kMore && rank == c.top_k - 1);
+      const double kth_key = readlane_f64(k, __builtin_ctzll(kth));
+      const double rest = BIAS ? (double)key_high(last, index_mask) : (double)of_order(last | index_mask);
+      const bool whole = last == 0 || (last & ~index_mask) == (order_of(-kInf) & ~index_mask);
+      int id = 0;
+      if (whole || kth_key > rest) {
+        for (int i = 0; i < c.top_k + kMore; ++i) {
+          const int to = __builtin_amdgcn_readlane(rank, i), oc = __builtin_amdgcn_readlane(cand, i);
+          if (lane == to) id = oc;
+        }
+      } else {
+        id = route64(row, c, stay, lane);
+      }
+      mine = index_mask - (uint32_t)id;
+    }
+  }
+  const int id = (int)(index_mask - (mine & index_mask));
+
+  // the weights
+  float my_x = -kInf;
+  if (lane < c.top_k) {
+    my_x = row.logit(id);
+    if (BIAS && !(bias[id] > -kInf)) my_x = -kInf;  // masked: weight 0
+  }
+  double w = 0.0;
+  // renormalised softmax weights need no more than the chosen experts' ratios
+  const float ref = SIGMOID ? 0.f : c.renormalize ? of_order(wave_max(order_of(my_x))) : row.top;
+  const float arg = SIGMOID ? my_x : my_x - ref;
+  if (__ballot(my_x != -kInf && arg < -80.f)) {  // near or past the end of binary32
+    if (my_x != -kInf) w = SIGMOID ? sigmoid64((double)my_x) : exp((double)my_x - (double)ref);
+  } else if (my_x != -kInf) {
+    w = SIGMOID ? rcp64(1.0 + (double)expf(-my_x)) : exp_diff(my_x, ref);
+  }
+  if (c.renormalize) {
+    row.sum64 = w;
+    for (int m = 1; m < c.top_k; m <<= 1) row.sum64 += __shfl_xor(row.sum64, m);
+  } else if (!SIGMOID) {
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) sum += x[j] == -kInf ? 0.0 : exp_diff(x[j], row.top);
+    row.sum64 = wave_sum(sum);
+  }
+  if (c.renormalize || !SIGMOID) w = row.sum64 > 0.0 ? w * rcp64(row.sum64) : 0.0;
+  if (lane < c.top_k) {
+    ids[t * c.top_k + lane] = id;
+    weights[t * c.top_k + lane] = (float)(w * (double)c.scale);
   }
 }
 
@@ -495,7 +497,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
 
 hipError_t launch_moe_route(const qdg_route_config& c, const void* logits, int64_t ld, const float* bias, int64_t T,
                             int32_t* ids, float* weights, uint32_t* status, hipStream_t s) {
-  const dim3 grid((unsigned)std::min<int64_t>((T + kWavesPerBlock - 1) / kWavesPerBlock, 1 << 14));
+  const dim3 grid((unsigned)((T + kWavesPerBlock - 1) / kWavesPerBlock));
   int epl = 1;
   while (epl * 64 < c.num_experts) epl *= 2;
   const size_t esz = c.ltype == QDG_L_F32 ? 4 : 2, load = std::min<size_t>(16, epl * esz);
@@ -511,12 +513,22 @@ hipError_t launch_moe_route(const qdg_route_config& c, const void* logits, int64
                        index_mask, ids, weights, status);
     return hipGetLastError();
   };
+  // one instance for each score, with and without bias and groups: a single
+  // one for all spilled scalar registers (8192 x 256 grouped 18.0 us)
+  auto pick = [&](auto experts_per_lane) {
+    constexpr int N = decltype(experts_per_lane)::value;
+    const bool sg = c.score == QDG_SCORE_SIGMOID, gr = c.num_groups > 1;
+    if (sg && bias) return gr ? go(moe_route_kernel<N, true, true, true>) : go(moe_route_kernel<N, true, true, false>);
+    if (sg) return gr ? go(moe_route_kernel<N, true, false, true>) : go(moe_route_kernel<N, true, false, false>);
+    if (bias) return gr ? go(moe_route_kernel<N, false, true, true>) : go(moe_route_kernel<N, false, true, false>);
+    return gr ? go(moe_route_kernel<N, false, false, true>) : go(moe_route_kernel<N, false, false, false>);
+  };
   switch (epl) {
-    case 1: return go(moe_route_kernel<1>);
-    case 2: return go(moe_route_kernel<2>);
-    case 4: return go(moe_route_kernel<4>);
-    case 8: return go(moe_route_kernel<8>);
-    default: return go(moe_route_kernel<16>);
+    case 1: return pick(std::integral_constant<int, 1>());
+    case 2: return pick(std::integral_constant<int, 2>());
+    case 4: return pick(std::integral_constant<int, 4>());
+    case 8: return pick(std::integral_constant<int, 8>());
+    default: return pick(std::integral_constant<int, 16>());
   }
 }
 
