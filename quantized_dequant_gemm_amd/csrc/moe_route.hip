@@ -14,7 +14,7 @@
 // reductions for all experts take twice the time (8192 tokens x 256 experts
 // in groups: 31 us). So the top_k + 1 largest are taken in binary32 and the
 // gaps between neighbours are compared with what the keys can be off by. Where
-// a gap does not decide (some 4 % of the tokens of normal logits and biases), eight
+// a gap does not decide (some 4 % of the tokens of normal logits and biases), four
 // more candidates are taken and ranked by binary64 keys, one lane each; if
 // not even these hold the top_k for sure, the whole token is routed in binary64.
 // Without a bias the keys are the logits: exact for 16-bit types, cut by the
@@ -25,8 +25,8 @@
 // adds 2^-24 + 2^-23 and passes on s (1 - s) of t's error, and s (1 - s) |x|
 // < 0.3: off by less than 2^-21 absolute. Softmax subtracts first (|d| 2^-24
 // more, s |d| < 0.4) and divides by a sum whose terms with mass have |d|
-// below about ln(1024): less than 2^-20. kScoreErr = 2^-19 for both, and the
-// bias added rounds by 2^-24 of the key.
+// below about ln(1024): less than 2^-20. score_err is twice that, and the bias
+// added rounds by 2^-24 of the key.
 //
 // The weights of the top_k, one lane each: exp in binary32 (one unit in the
 // last place, 2^-23) of the argument's upper part, times 1 + its lower part;
@@ -44,8 +44,7 @@ constexpr double kNegInf64 = -__builtin_inf();
 constexpr float kInf = __builtin_inff();
 constexpr float kMax = 3.402823466e+38f;  // largest finite
 constexpr int kWavesPerBlock = 4;
-constexpr float kScoreErr = 0x1p-19f;
-constexpr int kMore = 8;  // candidates beyond top_k where the order is in doubt
+constexpr int kMore = 4;  // candidates beyond top_k where the order is in doubt
 
 // One step of a maximum over the wave: lanes without a source, and rows
 // outside ROW_MASK, see 0.
@@ -186,27 +185,41 @@ struct Row {
 };
 
 // Which groups stay, decided on binary64 values (two groups' intervals
-// overlap at the border): a bit for each group.
-__device__ __forceinline__ uint64_t groups64(Row& row, const qdg_route_config& c, int lane) {
+// overlap at the border): a bit for each group. A group is 2^group_shift lanes
+// of epl experts, or (group_shift < 0) any run, which the whole wave walks.
+__device__ __forceinline__ uint64_t groups64(Row& row, const qdg_route_config& c, int epl, int group_shift, int lane) {
   const int G = c.num_groups, per = c.num_experts / G;
   if (row.score == QDG_SCORE_SOFTMAX) row.set_sum(lane);
+  auto add = [](double& m1, double& m2, double k) {
+    m2 = fmax(m2, fmin(m1, k));
+    m1 = fmax(m1, k);
+  };
+  auto merge = [](double& m1, double& m2, int m) {
+    const double o1 = __shfl_xor(m1, m), o2 = __shfl_xor(m2, m);
+    m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+    m1 = fmax(m1, o1);
+  };
+  auto value = [&](double m1, double m2) {
+    return c.group_score == QDG_GROUP_MAX || m2 == kNegInf64 ? m1 : m1 + m2;
+  };
   double mine = kNegInf64;  // lane g: the value of group g
-#pragma unroll 1
-  for (int g = 0; g < G; ++g) {
+  if (group_shift >= 0) {
     double m1 = kNegInf64, m2 = kNegInf64;
 #pragma unroll 1
-    for (int i = lane; i < per; i += 64) {
-      const double k = row.key64(g * per + i);
-      m2 = fmax(m2, fmin(m1, k));
-      m1 = fmax(m1, k);
-    }
+    for (int e = lane * epl; e < min((lane + 1) * epl, c.num_experts); ++e) add(m1, m2, row.key64(e));
 #pragma unroll 1
-    for (int m = 32; m > 0; m >>= 1) {
-      const double o1 = __shfl_xor(m1, m), o2 = __shfl_xor(m2, m);
-      m2 = fmax(fmin(m1, o1), fmax(m2, o2));
-      m1 = fmax(m1, o1);
+    for (int m = 1; m < 1 << group_shift; m <<= 1) merge(m1, m2, m);
+    mine = __shfl(value(m1, m2), (lane << group_shift) & 63);
+  } else {
+#pragma unroll 1
+    for (int g = 0; g < G; ++g) {
+      double m1 = kNegInf64, m2 = kNegInf64;
+#pragma unroll 1
+      for (int i = lane; i < per; i += 64) add(m1, m2, row.key64(g * per + i));
+#pragma unroll 1
+      for (int m = 32; m > 0; m >>= 1) merge(m1, m2, m);
+      if (lane == g) mine = value(m1, m2);
     }
-    if (lane == g) mine = c.group_score == QDG_GROUP_MAX || m2 == kNegInf64 ? m1 : m1 + m2;
   }
   int rank = 0;
 #pragma unroll 1
@@ -272,14 +285,17 @@ __device__ __forceinline__ uint32_t take_largest(uint32_t (&o)[EPL]) {
   return m;
 }
 
+// What a binary32 score is off by at most.
+__device__ __forceinline__ constexpr float score_err(bool sigmoid) { return sigmoid ? 0x1p-20f : 0x1p-19f; }
+
 // Bounds of the exact key behind an ordered one whose low bits are cut.
-__device__ __forceinline__ float key_low(uint32_t o, uint32_t index_mask) {
+__device__ __forceinline__ float key_low(uint32_t o, uint32_t index_mask, float err) {
   const float k = of_order(o & ~index_mask);
-  return k - kScoreErr - fabsf(k) * 0x1p-23f;
+  return k - err - fabsf(k) * 0x1p-23f;
 }
-__device__ __forceinline__ float key_high(uint32_t o, uint32_t index_mask) {
+__device__ __forceinline__ float key_high(uint32_t o, uint32_t index_mask, float err) {
   const float k = of_order(o | index_mask);
-  return k + kScoreErr + fabsf(k) * 0x1p-23f;
+  return k + err + fabsf(k) * 0x1p-23f;
 }
 
 // exp(a - b) for a <= b in binary64 with binary32's relative error 2^-23,
@@ -380,7 +396,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
     }
     float v = c.group_score == QDG_GROUP_MAX || m2 == -kInf ? m1 : m1 + m2;
     // two keys' errors and the roundings of keys and sum
-    const float err = fabsf(v) < kInf ? 2.f * kScoreErr + (fabsf(m1) + (m2 == -kInf ? 0.f : fabsf(m2))) * 0x1p-22f : 0.f;
+    const float err = fabsf(v) < kInf ? 2.f * score_err(SIGMOID) + (fabsf(m1) + (m2 == -kInf ? 0.f : fabsf(m2))) * 0x1p-22f : 0.f;
     v = __shfl(v, owner & 63);
     const float dv = __shfl(err, owner & 63);
     const float vl = v - dv, vu = v + dv;
@@ -392,7 +408,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
     }
     const bool in = lane < G && maybe < c.topk_groups;
     stay = __ballot(in);
-    if (__popcll(stay) != c.topk_groups) stay = groups64(row, c, lane);
+    if (__popcll(stay) != c.topk_groups) stay = groups64(row, c, EPL, group_shift, lane);
   }
 
   // the ordered keys
@@ -423,7 +439,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
     // does each gap to the next decide?
     const uint32_t next = (uint32_t)__shfl_down((int)mine, 1);
     const bool checked = lane < c.top_k && next != 0 && (mine & ~index_mask) != (order_of(-kInf) & ~index_mask);
-    const bool sure = BIAS ? key_low(mine, index_mask) > key_high(next, index_mask)
+    const bool sure = BIAS ? key_low(mine, index_mask, score_err(SIGMOID)) > key_high(next, index_mask, score_err(SIGMOID))
                            : (mine ^ next) > index_mask;  // exact but for the cut bits
     if (__ballot(checked && !sure)) {
       // kMore candidates more, ranked by binary64 keys, one lane each
@@ -446,7 +462,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
       // what was not taken is at most `last`; masked experts follow the index
       const uint64_t kth = __ballot(lane < c.top_k + kMore && rank == c.top_k - 1);
       const double kth_key = readlane_f64(k, __builtin_ctzll(kth));
-      const double rest = BIAS ? (double)key_high(last, index_mask) : (double)of_order(last | index_mask);
+      const double rest = BIAS ? (double)key_high(last, index_mask, score_err(SIGMOID)) : (double)of_order(last | index_mask);
       const bool whole = last == 0 || (last & ~index_mask) == (order_of(-kInf) & ~index_mask);
       int id = 0;
       if (whole || kth_key > rest) {
