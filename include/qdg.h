@@ -591,7 +591,8 @@ qdg_status qdg_quantize_act_zp(const void* a_bf16, int64_t lda, int64_t M, int64
                                float* a_scales, int32_t* a_zeros, void* stream);
 
 /* A layer of the direct int8 product. B i8 [num_experts][n][k], rows of ldb
-   bytes, experts n * ldb bytes apart; lda and ldb multiples of 16, >= k, <= 2^28; Y
+   bytes, experts n * ldb bytes apart; lda and ldb multiples of 16 (fastest: of
+   128), >= k, <= 2^28; Y
    rows of ldy elements, >= its columns (n, or n / 2 with QDG_EPI_SILU_MUL).
    otype BF16, F32, or I32 (the exact integers; scales and bias are ignored
    and may be NULL; not with an epilogue). epilogue QDG_EPI_NONE or

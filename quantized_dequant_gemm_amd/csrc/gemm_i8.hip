@@ -292,8 +292,12 @@ __device__ __forceinline__ void i8_frag_mma(const I8Frag<TM, TN>& f, i32x16_t (&
 #pragma unroll
   for (int i = FROM; i < TO; ++i) {
     const int t = i / TM, m = i % TM;
-    if (ZP && m == 0) zs[t] = i8_sum16(f.b[t], zs[t]);
     acc[m][t] = mfma_i8_32(f.b[t], f.a[m], acc[m][t]);
+    if constexpr (ZP) {  // the column sums' dot products, spread over the tile's MFMAs
+#pragma unroll
+      for (int d = 4 * m / TM; d < 4 * (m + 1) / TM; ++d)
+        zs[t] = __builtin_amdgcn_sdot4((int)f.b[t][d], 0x01010101, zs[t], false);
+    }
   }
 }
 
@@ -491,8 +495,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   int g = g0;
   // full rounds of NS groups with constant stages, then the rest, the last
   // group cut at k
-  if constexpr (TM * TN <= 4) {
-    static_assert(NS % 2 == 0, "the two fragment sets alternate with the stages");
+  if constexpr (TM * TN <= 4 && NS % 2 == 0) {  // the two fragment sets alternate with the stages
     I8Frag<TM, TN> f[2][4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) i8_frag_load(f[0][q], st0, a_lane, b_lane, at[q]);
@@ -672,23 +675,31 @@ hipError_t launch_tile(const I8Args& a, bool silu, int m_blocks, int split, hipS
 }
 
 // ------------------------------------------------------------- dense choice
-// A dense product runs the rows kernel or one of four tiles, its K perhaps
-// split over workgroups. Measured on MI355X with the tiles filling the card
-// once: microseconds for one 128-byte group of K, and for a round's prologue
-// and epilogue. A product of R rounds of tiles over G groups takes about
-// R (G group + round) + 3 us (M = 256, n = 14336, k = 4096: 64 x 64 29 us, 128 x 64
-// 26, 128 x 128 22; M = n = k = 4096: 128 x 128 79, 256 x 256 66). A split adds a second kernel and the
-// partials' traffic (M = 64, n = 512, k = 16384: 25.4 us whole, 7.6 + 4.2 us in eight).
-enum I8Kernel { I8_ROWS, I8_64X64, I8_128X64, I8_128X128, I8_256X256 };
+// A dense product runs the rows kernel or one of five tiles, its K perhaps
+// split over workgroups, by a time model: R rounds of tiles over G groups
+// take R (G group + round) + 3 us. group: measured microseconds for a
+// 128-byte group of K with the tiles filling the card once, and (many) where
+// several rounds of tiles no longer find their operands in L2; round: a
+// round's prologue and epilogue. Measured in microseconds, bf16 output:
+//                    64x64  128x64  128x128  128x256  256x256
+//    256 x  4096 x 4096   10.9    15.6     20.1       37       53
+//    256 x 14336 x 4096     29      26       22       37       60
+//   1024 x  4096 x 4096     30      27       25       39       55
+//   2048 x  4096 x 4096     63      66       44       38       55
+//   4096 x  4096 x 4096                      93       83       66
+// A split adds a second kernel and the partials' traffic (64 x 512 x 16384,
+// 64 x 64: 25.4 us whole, 7.6 + 4.2 us in eight).
+enum I8Kernel { I8_ROWS, I8_64X64, I8_128X64, I8_128X128, I8_128X256, I8_256X256 };
 struct I8Tile {
   I8Kernel kernel;
   int bm, bn;
-  float group, round;
+  float group, many, round;
 };
-constexpr I8Tile kI8Tiles[] = {{I8_64X64, 64, 64, 0.19f, 1.f},
-                               {I8_128X64, 128, 64, 0.33f, 1.5f},
-                               {I8_128X128, 128, 128, 0.53f, 2.f},
-                               {I8_256X256, 256, 256, 1.67f, 4.f}};
+constexpr I8Tile kI8Tiles[] = {{I8_64X64, 64, 64, 0.19f, 0.27f, 1.f},
+                               {I8_128X64, 128, 64, 0.33f, 0.36f, 1.5f},
+                               {I8_128X128, 128, 128, 0.53f, 0.56f, 3.f},
+                               {I8_128X256, 128, 256, 1.07f, 1.07f, 4.f},
+                               {I8_256X256, 256, 256, 1.67f, 1.67f, 4.f}};
 constexpr int kCus = 256;
 
 I8Kernel choose_dense(int64_t M, int64_t vcols, int64_t k, bool silu, int* split) {
@@ -701,8 +712,8 @@ I8Kernel choose_dense(int64_t M, int64_t vcols, int64_t k, bool silu, int* split
     const int64_t tiles = (M + t.bm - 1) / t.bm * ((vcols + t.bn - 1) / t.bn);
     for (int s = 1; s <= 8; s *= 2) {
       if (s > 1 && (tiles * s > kCus || groups < 8 * s)) break;
-      const float rounds = (float)((tiles * s + kCus - 1) / kCus);
-      float us = rounds * ((float)((groups + s - 1) / s) * t.group + t.round) + 3.f;
+      const int64_t rounds = (tiles * s + kCus - 1) / kCus;
+      float us = (float)rounds * ((float)((groups + s - 1) / s) * (rounds > 1 ? t.many : t.group) + t.round) + 3.f;
       if (s > 1) us += 5.f + (float)(M * vcols * s) * 8e-6f / 4.f;  // written and read at about 4 TB/s
       if (best_us == 0.f || us < best_us) {
         best_us = us;
@@ -739,6 +750,7 @@ hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s) {
     }
     case I8_64X64: e = launch_tile<2, 2, 1, 1, 4, false>(a, silu, (a.M + 63) / 64, split, s); break;
     case I8_128X64: e = launch_tile<4, 2, 1, 1, 4, false>(a, silu, (a.M + 127) / 128, split, s); break;
+    case I8_128X256: e = launch_tile<2, 4, 2, 2, 3, false>(a, silu, (a.M + 127) / 128, split, s); break;
     case I8_128X128: e = launch_tile<2, 4, 2, 1, 4, false>(a, silu, (a.M + 127) / 128, split, s); break;
     default: e = launch_tile<2, 4, 4, 2, 2, false>(a, silu, (a.M + 255) / 256, split, s); break;
   }
