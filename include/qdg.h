@@ -618,7 +618,8 @@ qdg_status qdg_gemm_i8_workspace(const qdg_i8_config* cfg, int64_t M, size_t* by
    [-128, 127], or NULL (all 0); b_scales f32 [n]; bias f32 [n] or NULL. A and
    B 16-byte aligned, the others aligned to their elements; workspace 16-byte
    aligned, NULL where none is needed. Bytes of A and B rows behind k may hold
-   anything. M in [0, 2^26] (0 enqueues nothing). Row m of Y does not depend
+   anything. M in [0, 2^26] (0 enqueues nothing). QDG_ERR_UNSUPPORTED also
+   where Y has more tiles than one launch holds (at least 2^28 elements). Row m of Y does not depend
    on M or on the other rows, and results are the same on every call. */
 qdg_status qdg_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const float* a_scales, const int32_t* a_zeros,
                        const int8_t* B, const float* b_scales, const float* bias, void* Y, int64_t M,

@@ -27,6 +27,13 @@ qdg_status hip_status(hipError_t e, const char* what) {
   return fail(QDG_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
+// hipErrorInvalidConfiguration: the launcher found more tiles than a launch holds.
+qdg_status i8_launch_status(hipError_t e, const char* what) {
+  if (e == hipErrorInvalidConfiguration)
+    return fail(QDG_ERR_UNSUPPORTED, "%s: the output has more tiles than one launch holds (2^32 threads)", what);
+  return hip_status(e, what);
+}
+
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
@@ -181,7 +188,7 @@ qdg_status qdg_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const float* a
     if (!aligned(workspace, 16)) return fail(QDG_ERR_MISALIGNED, "workspace must be 16-byte aligned");
     a.partial = (int32_t*)workspace;
   }
-  return hip_status(launch_gemm_i8(a, cfg->epilogue == QDG_EPI_SILU_MUL, (hipStream_t)stream),
+  return i8_launch_status(launch_gemm_i8(a, cfg->epilogue == QDG_EPI_SILU_MUL, (hipStream_t)stream),
                     "gemm_i8 launch");
 }
 
@@ -211,7 +218,7 @@ qdg_status qdg_moe_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const floa
   a.block_m = block_m;
   if ((int64_t)a.M * a.lda > (int64_t)kI8FarRow)
     return fail(QDG_ERR_UNSUPPORTED, "A is longer than 3.75 GiB: route fewer tokens at a time");
-  return hip_status(launch_moe_gemm_i8(a, cfg->epilogue == QDG_EPI_SILU_MUL, (int)(capacity / block_m),
+  return i8_launch_status(launch_moe_gemm_i8(a, cfg->epilogue == QDG_EPI_SILU_MUL, (int)(capacity / block_m),
                                        (hipStream_t)stream),
                     "moe_gemm_i8 launch");
 }

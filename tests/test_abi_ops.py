@@ -118,6 +118,13 @@ def test_moe_refusals():
     assert _moe(A=None) == inv and _moe(Y=None) == inv and _moe(B=P + 4) == mis
 
 
+def test_more_tiles_than_a_launch_holds():
+    """2^20 pairs in 16-row blocks and 2^16 columns: refused before anything is enqueued."""
+    cfg = q.gemm_i8(1 << 16, 64, num_experts=8)
+    assert _status(q.qdg_moe_gemm_i8, cfg, P, P, P, P, P, P, P, P, P, 1 << 19, 2, 16, 0, P) == q.QDG_ERR_UNSUPPORTED
+    assert _gemm(M=1 << 26, n=1 << 20, k=16) == q.QDG_ERR_UNSUPPORTED
+
+
 def test_messages_name_the_cause():
     with pytest.raises(q.QdgError, match="num_groups must divide"):
         q.qdg_moe_route(q.route(64, 4, num_groups=3), P, 64, None, 1, P, P)

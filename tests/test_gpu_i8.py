@@ -134,6 +134,33 @@ def test_long_k_with_few_columns(qdg, M, n, k):
     _close(_dense(L, q.QDG_O_F32, q.QDG_EPI_SILU_MUL), y64, err, False)
 
 
+@pytest.mark.parametrize("M,n,k", [(5, 40, 200), (70, 200, 300), (60, 128, 16400)])
+def test_raw_output_reads_no_scales(qdg, M, n, k):
+    L = Layer(np.random.default_rng(3), M, n, k, zeros=True, bias=False)
+    cfg = L.cfg(q.QDG_O_I32, q.QDG_EPI_NONE)
+    y = torch.zeros((M, n), dtype=torch.int32, device="cuda")
+    nbytes = q.qdg_gemm_i8_workspace(cfg, M)
+    ws = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device="cuda")
+    q.qdg_gemm_i8(cfg, L.dA.data_ptr(), None, L.dza.data_ptr(), L.dB.data_ptr(), None, None, y.data_ptr(), M,
+                  ws.data_ptr(), nbytes, q.current_stream())
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(y.cpu().numpy(), ops.int_product(L.a, L.b[0], L.za))
+
+
+def test_every_tile_and_a_split_at_odd_sizes(qdg):
+    """Sizes for which the time model takes each kernel: rows, 64 x 64 (whole and split), 128 x 64, 128 x 128,
+    128 x 256 and 256 x 256 tiles; every row and column is compared."""
+    assert q.qdg_gemm_i8_workspace(q.gemm_i8(500, 16385), 33) > 0  # the split
+    for M, n, k in ((16, 4099, 130), (33, 500, 16385), (200, 1030, 515), (130, 4100, 2050), (257, 7300, 1030),
+                    (513, 14337, 700), (2049, 4099, 1027), (4097, 5000, 515)):
+        rng = np.random.default_rng(M)
+        L = Layer(rng, M, n, k, zeros=True, bias=False)
+        a = L.dA[:, :k].float() - L.dza.float()[:, None]
+        want = (a.double() @ L.dB[:, :k].double().t()).to(torch.int32)
+        got = _dense(L, q.QDG_O_I32, pad_y=3)
+        assert torch.equal(got, want), (M, n, k)
+
+
 def test_rows_do_not_depend_on_the_batch(qdg):
     rng = np.random.default_rng(21)
     L = Layer(rng, 300, 384, 1000, zeros=True, bias=True)
