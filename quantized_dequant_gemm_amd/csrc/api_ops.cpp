@@ -99,7 +99,7 @@ qdg_status i8_args(const qdg_i8_config* c, const int8_t* A, const float* a_scale
 size_t i8_workspace(const qdg_i8_config* c, int64_t M) {
   const bool silu = c->epilogue == QDG_EPI_SILU_MUL;
   const int64_t vcols = gemm_i8_vcols(silu ? c->n / 2 : c->n, silu);
-  const int split = M > 0 ? gemm_i8_split(M, vcols, c->k, silu) : 1;
+  const int split = M > 0 ? gemm_i8_split(M, vcols, c->k) : 1;
   return split > 1 ? (size_t)split * (size_t)M * (size_t)vcols * sizeof(int32_t) : 0;
 }
 

@@ -212,8 +212,8 @@ __global__ __launch_bounds__(256) void gemm_i8_reduce_kernel(const I8Args p, int
 // different banks without padding.
 //
 // What bounds them: the 256 x 256 tile the card's power (8192^3: 2.3-2.4 POP/s
-// with random codes, 3.1 with A all zero; 4096 x 14336 x 4096 250 us = 1.9 POP/s,
-// 3.5 rounds of tiles in 4); the small tiles the copies into LDS (16-20 TB/s
+// with random codes, 3.1 with A all zero; 4096 x 14336 x 4096 239-247 us = 2.0
+// POP/s); the small tiles the copies into LDS (16-20 TB/s
 // over the card, so a 64 x 64 tile takes 0.19 us a group where its MFMAs take 0.06);
 // with up to 64 rows HBM (16 x 14336 x 4096 12.3 us = 4.8 TB/s). Row strides
 // that are no multiple of 128 bytes split every copied piece over two lines:
@@ -449,7 +449,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   };
   // 16-column tiles of B in the order the epilogue wants (gate and up tiles
   // alternate with SILU)
-  const int vt0 = nb * (BN / 16);
+  const int vt0 = p.vt_first + nb * (BN / 16);
   I8Src<LOADS> src;
   const int64_t k16 = (p.k + 15) / 16 * 16;
 #pragma unroll
@@ -660,9 +660,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
 }
 
 template <int WM, int WN, int TM, int TN, int NS, bool MOE>
-hipError_t launch_tile(const I8Args& a, bool silu, int m_blocks, int split, hipStream_t s) {
+hipError_t launch_tile(const I8Args& a, bool silu, int m_blocks, int split, hipStream_t s, int n_limit = 0) {
   constexpr int BN = 32 * TN * WN, THREADS = 64 * WM * WN;
-  const int n_blocks = (a.vcols + BN - 1) / BN;
+  const int n_blocks = n_limit ? n_limit : (a.vcols - a.vt_first * 16 + BN - 1) / BN;
   int64_t blocks = (int64_t)m_blocks * n_blocks;
   int m_run = 1;
   if (MOE) {
@@ -712,65 +712,95 @@ constexpr I8Tile kI8Tiles[] = {{I8_64X64, 64, 64, 0.19f, 0.27f, 1.f},
                                {I8_256X256, 256, 256, 1.67f, 1.67f, 4.f}};
 constexpr int kCus = 256;
 
-I8Kernel choose_dense(int64_t M, int64_t vcols, int64_t k, bool silu, int* split) {
-  *split = 1;
-  if (M <= 16 && vcols < 8192) return I8_ROWS;
+int64_t i8_rounds(int64_t tiles) { return (tiles + kCus - 1) / kCus; }
+
+float i8_rounds_us(const I8Tile& t, int64_t tiles, int64_t groups) {
+  const int64_t rounds = i8_rounds(tiles);
+  return (float)rounds * ((float)groups * (rounds > 1 ? t.many : t.group) + t.round);
+}
+
+// The tiles (kernel, its K in split parts) of the columns up to n_main column
+// blocks, and with n_main > 0 another tile (rest, whole K) behind them.
+struct I8Choice {
+  I8Kernel kernel, rest;
+  int split, n_main;
+};
+
+I8Choice choose_dense(int64_t M, int64_t vcols, int64_t k) {
+  if (M <= 16 && vcols < 8192) return {I8_ROWS, I8_ROWS, 1, 0};
   const int64_t groups = (k + 127) / 128;
-  I8Kernel best = I8_64X64;
+  I8Choice best = {I8_64X64, I8_64X64, 1, 0};
   float best_us = 0.f;
   for (const I8Tile& t : kI8Tiles) {
-    const int64_t tiles = (M + t.bm - 1) / t.bm * ((vcols + t.bn - 1) / t.bn);
+    const int64_t m_blocks = (M + t.bm - 1) / t.bm, n_blocks = (vcols + t.bn - 1) / t.bn, tiles = m_blocks * n_blocks;
     for (int s = 1; s <= 8; s *= 2) {
       if (s > 1 && (tiles * s > kCus || groups < 8 * s)) break;
-      const int64_t rounds = (tiles * s + kCus - 1) / kCus;
-      float us = (float)rounds * ((float)((groups + s - 1) / s) * (rounds > 1 ? t.many : t.group) + t.round) + 3.f;
+      float us = i8_rounds_us(t, tiles * s, (groups + s - 1) / s) + 3.f;
       if (s > 1) us += 5.f + (float)(M * vcols * s) * 8e-6f / 4.f;  // written and read at about 4 TB/s
       if (best_us == 0.f || us < best_us) {
         best_us = us;
-        best = t.kernel;
-        *split = s;
+        best = {t.kernel, t.kernel, s, 0};
+      }
+    }
+    // Whole rounds of this tile, and what the last round would hold of it in
+    // smaller ones: 4096 x 14336 x 4096 is 3.5 rounds of 256 x 256 tiles
+    // (259 us in four, 247 with the rest in 128 x 256), 4096 x 4608 x 4096 1.1 (120, 86 us)
+    const int64_t full = tiles / kCus, n_main = m_blocks > 0 ? full * kCus / m_blocks : 0;
+    if (tiles % kCus == 0 || n_main < 1 || n_main >= n_blocks) continue;
+    for (const I8Tile& r : kI8Tiles) {
+      const int64_t rest = (M + r.bm - 1) / r.bm * ((vcols - n_main * t.bn + r.bn - 1) / r.bn);
+      const float us = i8_rounds_us(t, m_blocks * n_main, groups) + i8_rounds_us(r, rest, groups) + 5.f;
+      if (us < best_us) {
+        best_us = us;
+        best = {t.kernel, r.kernel, 1, (int)n_main};
       }
     }
   }
   return best;
 }
 
+hipError_t launch_dense_tile(I8Kernel kernel, const I8Args& a, bool silu, int split, hipStream_t s, int n_limit) {
+  switch (kernel) {
+    case I8_64X64: return launch_tile<2, 2, 1, 1, 4, false>(a, silu, (a.M + 63) / 64, split, s, n_limit);
+    case I8_128X64: return launch_tile<4, 2, 1, 1, 4, false>(a, silu, (a.M + 127) / 128, split, s, n_limit);
+    case I8_128X128: return launch_tile<2, 4, 2, 1, 4, false>(a, silu, (a.M + 127) / 128, split, s, n_limit);
+    case I8_128X256: return launch_tile<2, 4, 2, 2, 3, false>(a, silu, (a.M + 127) / 128, split, s, n_limit);
+    default: return launch_tile<2, 4, 4, 2, 2, false>(a, silu, (a.M + 255) / 256, split, s, n_limit);
+  }
+}
+
 }  // namespace
 
 int64_t gemm_i8_vcols(int64_t cols, bool silu) { return (cols + 15) / 16 * 16 * (silu ? 2 : 1); }
 
-int gemm_i8_split(int64_t M, int64_t vcols, int64_t k, bool silu) {
-  int split;
-  choose_dense(M, vcols, k, silu, &split);
-  return split;
-}
+int gemm_i8_split(int64_t M, int64_t vcols, int64_t k) { return choose_dense(M, vcols, k).split; }
 
 hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s) {
-  int split;
-  hipError_t e;
-  switch (choose_dense(a.M, a.vcols, a.k, silu, &split)) {
-    case I8_ROWS: {
-      const dim3 grid((unsigned)((a.cols + 15) / 16));
-      auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(512), 0, s, a);
-        return hipGetLastError();
-      };
-      if (silu) return a.a_zeros ? go(gemm_i8_rows_kernel<8, true, true>) : go(gemm_i8_rows_kernel<8, true, false>);
-      return a.a_zeros ? go(gemm_i8_rows_kernel<8, false, true>) : go(gemm_i8_rows_kernel<8, false, false>);
-    }
-    case I8_64X64: e = launch_tile<2, 2, 1, 1, 4, false>(a, silu, (a.M + 63) / 64, split, s); break;
-    case I8_128X64: e = launch_tile<4, 2, 1, 1, 4, false>(a, silu, (a.M + 127) / 128, split, s); break;
-    case I8_128X256: e = launch_tile<2, 4, 2, 2, 3, false>(a, silu, (a.M + 127) / 128, split, s); break;
-    case I8_128X128: e = launch_tile<2, 4, 2, 1, 4, false>(a, silu, (a.M + 127) / 128, split, s); break;
-    default: e = launch_tile<2, 4, 4, 2, 2, false>(a, silu, (a.M + 255) / 256, split, s); break;
+  const I8Choice c = choose_dense(a.M, a.vcols, a.k);
+  if (c.kernel == I8_ROWS) {
+    const dim3 grid((unsigned)((a.cols + 15) / 16));
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(512), 0, s, a);
+      return hipGetLastError();
+    };
+    if (silu) return a.a_zeros ? go(gemm_i8_rows_kernel<8, true, true>) : go(gemm_i8_rows_kernel<8, true, false>);
+    return a.a_zeros ? go(gemm_i8_rows_kernel<8, false, true>) : go(gemm_i8_rows_kernel<8, false, false>);
   }
-  if (e != hipSuccess || split <= 1) return e;
+  hipError_t e = launch_dense_tile(c.kernel, a, silu, c.split, s, c.n_main);
+  if (e != hipSuccess) return e;
+  if (c.n_main > 0) {
+    I8Args rest = a;
+    for (const I8Tile& t : kI8Tiles)
+      if (t.kernel == c.kernel) rest.vt_first = c.n_main * (t.bn / 16);
+    return launch_dense_tile(c.rest, rest, silu, 1, s, 0);
+  }
+  if (c.split <= 1) return e;
   const int64_t threads = (int64_t)a.M * ((a.cols + 3) / 4);
   const dim3 grid((unsigned)((threads + 255) / 256));
   if (silu)
-    hipLaunchKernelGGL(gemm_i8_reduce_kernel<true>, grid, dim3(256), 0, s, a, split);
+    hipLaunchKernelGGL(gemm_i8_reduce_kernel<true>, grid, dim3(256), 0, s, a, c.split);
   else
-    hipLaunchKernelGGL(gemm_i8_reduce_kernel<false>, grid, dim3(256), 0, s, a, split);
+    hipLaunchKernelGGL(gemm_i8_reduce_kernel<false>, grid, dim3(256), 0, s, a, c.split);
   return hipGetLastError();
 }
 

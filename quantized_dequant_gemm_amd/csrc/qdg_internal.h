@@ -175,6 +175,7 @@ struct I8Args {
   int cols;                // columns of Y (n, or n / 2 with the SiLU*mul epilogue)
   int otype;
   int vcols;               // columns of B's tiles in the kernels' order, whole tiles (gemm_i8_vcols)
+  int vt_first;            // the 16-column tile of B that the launch starts at
   int32_t* partial;        // split K: int32 partials [split][M][vcols]
   // grouped by expert (sorted_ids NULL: dense)
   const int32_t* sorted_ids;
@@ -186,7 +187,7 @@ struct I8Args {
 // with 32 bits, and rows that are not there behind it)
 constexpr uint32_t kI8FarRow = 0xF0000000u;
 int64_t gemm_i8_vcols(int64_t cols, bool silu);
-int gemm_i8_split(int64_t M, int64_t vcols, int64_t k, bool silu);
+int gemm_i8_split(int64_t M, int64_t vcols, int64_t k);
 hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s);
 hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int m_blocks, hipStream_t s);
 

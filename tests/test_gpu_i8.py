@@ -152,13 +152,26 @@ def test_every_tile_and_a_split_at_odd_sizes(qdg):
     128 x 256 and 256 x 256 tiles; every row and column is compared."""
     assert q.qdg_gemm_i8_workspace(q.gemm_i8(500, 16385), 33) > 0  # the split
     for M, n, k in ((16, 4099, 130), (33, 500, 16385), (200, 1030, 515), (130, 4100, 2050), (257, 7300, 1030),
-                    (513, 14337, 700), (2049, 4099, 1027), (4097, 5000, 515)):
+                    (513, 14337, 700), (2049, 4099, 1027), (4097, 5000, 515), (4096, 4610, 900)):
         rng = np.random.default_rng(M)
         L = Layer(rng, M, n, k, zeros=True, bias=False)
         a = L.dA[:, :k].float() - L.dza.float()[:, None]
         want = (a.double() @ L.dB[:, :k].double().t()).to(torch.int32)
         got = _dense(L, q.QDG_O_I32, pad_y=3)
         assert torch.equal(got, want), (M, n, k)
+
+
+@pytest.mark.parametrize("epi", [q.QDG_EPI_NONE, q.QDG_EPI_SILU_MUL])
+def test_columns_behind_whole_rounds_of_tiles(qdg, epi):
+    """4096 x 4620 columns are one round of 256 x 256 tiles and a rest in another tile."""
+    M, n, k = 4096, 4620, 600
+    L = Layer(np.random.default_rng(9), M, n, k, zeros=True, bias=True)
+    L.sb /= np.float32(np.sqrt(k) * 5)
+    L.dsb = H.dev(L.sb)
+    y = _dense(L, q.QDG_O_F32, epi)
+    for rows in (slice(0, 40), slice(2040, 2080), slice(4060, 4096)):  # every column of these
+        y64, err = L.ref(epi, rows)
+        _close(y[rows], y64, err, False)
 
 
 def test_rows_do_not_depend_on_the_batch(qdg):
