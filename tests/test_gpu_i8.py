@@ -174,15 +174,47 @@ def test_columns_behind_whole_rounds_of_tiles(qdg, epi):
         _close(y[rows], y64, err, False)
 
 
-def test_rows_do_not_depend_on_the_batch(qdg):
+@pytest.mark.parametrize("epi", [q.QDG_EPI_NONE, q.QDG_EPI_SILU_MUL])
+def test_rows_do_not_depend_on_the_batch(qdg, epi):
     rng = np.random.default_rng(21)
     L = Layer(rng, 300, 384, 1000, zeros=True, bias=True)
-    full = _dense(L, q.QDG_O_F32)
+    full = _dense(L, q.QDG_O_F32, epi)
     for m in (1, 16, 40, 64, 65, 128, 200):
         S = Layer.__new__(Layer)
         S.__dict__.update(L.__dict__)
         S.M = m
-        assert torch.equal(_dense(S, q.QDG_O_F32), full[:m])
+        assert torch.equal(_dense(S, q.QDG_O_F32, epi), full[:m])
+
+
+def test_split_product_in_two_graphs(qdg):
+    """Two captured products with a workspace each, replayed in turn with eager work between."""
+    rng = np.random.default_rng(23)
+    sides = []
+    for M in (33, 40):
+        L = Layer(rng, M, 256, 16400, zeros=True, bias=True)
+        cfg = L.cfg(q.QDG_O_F32, q.QDG_EPI_NONE)
+        nbytes = q.qdg_gemm_i8_workspace(cfg, M)
+        assert nbytes > 0
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+        y = torch.zeros((M, 256), device="cuda")
+        want = _dense(L, q.QDG_O_F32).clone()
+        call = lambda st, L=L, cfg=cfg, ws=ws, y=y, nbytes=nbytes: q.qdg_gemm_i8(
+            cfg, L.dA.data_ptr(), L.dsa.data_ptr(), L.dza.data_ptr(), L.dB.data_ptr(), L.dsb.data_ptr(),
+            L.dbias.data_ptr(), y.data_ptr(), L.M, ws.data_ptr(), nbytes, st)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(q.current_stream())
+        sides.append((L, call, g, y, want))
+    for _ in range(4):
+        for L, call, g, y, want in sides:
+            y.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+            y.fill_(7.0)
+            call(q.current_stream())
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
 
 
 def test_unusual_scales(qdg):
