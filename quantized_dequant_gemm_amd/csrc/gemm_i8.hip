@@ -242,13 +242,18 @@ struct I8Src {
 };
 
 // The resource for rows from `row` on of an operand of `rows` rows, its last
-// row `len` bytes long.
+// row `len` bytes long. All of it is the same in every lane, and said to be: the
+// 64-bit comparisons run on the vector unit, and a resource left in vector
+// registers costs a loop around every copy.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t i8_rows_rsrc(const int8_t* base, int64_t row, int64_t rows,
                                                               int64_t ld, int64_t len) {
   int64_t left = (rows - 1 - row) * ld + len;
   left = left < 0 ? 0 : left > 0xFFFFFFFFll ? 0xFFFFFFFFll : left;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base + (left > 0 ? row * ld : 0)), (short)0,
-                                           (int)(uint32_t)left, 0x00020000);
+  const uint64_t at = (uint64_t)(base + (left > 0 ? row * ld : 0));
+  const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+  const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)(hi << 32 | lo), (short)0,
+                                           __builtin_amdgcn_readfirstlane((int)(uint32_t)left), 0x00020000);
 }
 
 // Copies FROM .. TO - 1 of group g into one stage (every wave issues the same
@@ -391,7 +396,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
                                                                      int m_run) {
   constexpr int NW = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN, BYTES = (BM + BN) * 128;
   constexpr int LOADS = (BM + BN) / 8 / NW, TAG = ((WM * 8 + WN) * 8 + TM) * 512 + (TN * 8 + NS) * 8 + SILU * 4 + ZP * 2 + MOE;
-  static_assert((BM + BN) / 8 % NW == 0, "every wave issues the same number of copies");
+  static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0, "every wave issues the same copies of A and of B");
+  constexpr int A_LOADS = BM / 8 / NW;
   static_assert(NS >= 2 && NS <= 8 && NS * BYTES <= 160 * 1024, "two to eight stages within LDS");
   static_assert(LOADS * (NS - 1) < 64, "vmcnt holds the copies in flight");
   // separate objects, so that the compiler can tell a copy into one stage
@@ -434,12 +440,6 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
       nb = lin % n_blocks;
     }
   }
-  int expert = 0;
-  if constexpr (MOE) {
-    if (mb * p.block_m >= *p.num_padded) return;
-    expert = p.block_expert[mb];
-    if ((unsigned)expert >= (unsigned)p.num_experts) return;
-  }
   // the pair behind a row of the tile, -1 for none (a 16-row block fills half
   // of a 32-row tile)
   auto pair_of = [&](int row) {
@@ -447,22 +447,59 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
     const int id = p.sorted_ids[mb * p.block_m + row];
     return (unsigned)id < (unsigned)p.num_pairs ? id : -1;
   };
+  auto a_row_of = [&](int pair) { return p.a_per_pair ? pair : pair / p.top_k; };
+  // What the epilogue needs of the rows and columns, and the rows of A, are
+  // asked for here at once: one after the other, and at the end, they cost a memory
+  // latency each.
+  constexpr int TC = SILU ? 16 : 32;  // columns of Y from a 32-column tile
+  const bool raw = p.otype == QDG_O_I32;
+  int expert = 0, a_pair[A_LOADS], yr[TM], za[TM];  // yr < 0: no row
+  float sa[TM];
+  if constexpr (MOE) {
+    const int used = __builtin_amdgcn_readfirstlane(*p.num_padded);
+    expert = __builtin_amdgcn_readfirstlane(p.block_expert[mb]);
+#pragma unroll
+    for (int q = 0; q < A_LOADS; ++q) a_pair[q] = pair_of((q * NW + wave) * 8 + (lane >> 3));
+#pragma unroll
+    for (int m = 0; m < TM; ++m) yr[m] = pair_of((wm * TM + m) * 32 + r);
+    if (mb * p.block_m >= used || (unsigned)expert >= (unsigned)p.num_experts) return;
+  } else {
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      yr[m] = mb * BM + (wm * TM + m) * 32 + r;
+      if (yr[m] >= p.M) yr[m] = -1;
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    const int ar = yr[m] < 0 ? 0 : MOE ? a_row_of(yr[m]) : yr[m];
+    sa[m] = raw ? 1.f : p.a_scales[ar];
+    za[m] = ZP ? p.a_zeros[ar] : 0;
+  }
   // 16-column tiles of B in the order the epilogue wants (gate and up tiles
   // alternate with SILU)
   const int vt0 = p.vt_first + nb * (BN / 16);
+  static_assert(BN <= 64 * NW, "a thread for every column");
+  float my_scale = 0.f, my_bias = 0.f;
+  if (!raw && threadIdx.x < BN) {
+    int first, rows;
+    i8_tile<SILU>(p, vt0 + threadIdx.x / 16, first, rows);
+    const int64_t at = (int64_t)expert * p.n + (rows > 0 ? first + min((int)threadIdx.x % 16, rows - 1) : 0);
+    my_scale = p.b_scales[at];
+    my_bias = p.bias ? p.bias[at] : 0.f;
+  }
   I8Src<LOADS> src;
   const int64_t k16 = (p.k + 15) / 16 * 16;
 #pragma unroll
   for (int q = 0; q < LOADS; ++q) {
     const int i = q * NW + wave;  // rows 8 i .. 8 i + 7 of the stage: A, then B
     const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3) ^ (i & 1)) * 16u;
-    if (i < BM / 8) {
+    if (q < A_LOADS) {
       if constexpr (MOE) {
-        const int id = pair_of(i * 8 + (lane >> 3));
         // A ends below kI8FarRow (checked by the host): rows that are not
         // there read zeros behind it
         src.rsrc[q] = i8_rows_rsrc(p.A, 0, p.M, p.lda, k16);
-        src.off[q] = id < 0 ? kI8FarRow : (uint32_t)(p.a_per_pair ? id : id / p.top_k) * (uint32_t)p.lda + chunk;
+        src.off[q] = a_pair[q] < 0 ? kI8FarRow : (uint32_t)a_row_of(a_pair[q]) * (uint32_t)p.lda + chunk;
       } else {
         src.rsrc[q] = i8_rows_rsrc(p.A, mb * BM + i * 8, p.M, p.lda, k16);
         src.off[q] = (uint32_t)(lane >> 3) * (uint32_t)p.lda + chunk;
@@ -553,15 +590,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   float* cbias = cscale + BN;
   int* zbuf = (int*)(cbias + BN) + wave * TN * 32;
   char* strip = (wave < NW / 2 ? st0 : st1) + wave % (NW / 2) * STRIP;
-  const bool raw = p.otype == QDG_O_I32;
-  if (!raw)
-    for (int c = threadIdx.x; c < BN; c += 64 * NW) {
-      int first, rows;
-      i8_tile<SILU>(p, vt0 + c / 16, first, rows);
-      const int64_t at = (int64_t)expert * p.n + (rows > 0 ? first + min(c % 16, rows - 1) : 0);
-      cscale[c] = p.b_scales[at];
-      cbias[c] = p.bias ? p.bias[at] : 0.f;
-    }
+  if (threadIdx.x < BN) {
+    cscale[threadIdx.x] = my_scale;
+    cbias[threadIdx.x] = my_bias;
+  }
   if constexpr (ZP) {
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
@@ -570,25 +602,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
     }
   }
   __syncthreads();
-  constexpr int TC = SILU ? 16 : 32;  // columns of Y from a 32-column tile
   const int wave_col = (vt0 * 16 + wn * TN * 32) / (SILU ? 2 : 1);
 #pragma unroll
   for (int m = 0; m < TM; ++m) {
-    int yr = mb * BM + (wm * TM + m) * 32 + r, ar = min(yr, p.M - 1);  // yr < 0: no row
-    if constexpr (MOE) {
-      yr = pair_of((wm * TM + m) * 32 + r);
-      ar = yr < 0 ? 0 : p.a_per_pair ? yr : yr / p.top_k;
-    } else if (yr >= p.M) {
-      yr = -1;
-    }
-    const int za = ZP ? p.a_zeros[ar] : 0;
-    const float sa = raw ? 1.f : p.a_scales[ar];
     auto sums = [&](int t, int q) {
       i32x4_t v;
       i32x4_t z = {0, 0, 0, 0};
       if constexpr (ZP) z = *(const i32x4_t*)(zbuf + t * 32 + q * 8 + half * 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = acc[m][t][q * 4 + i] - za * z[i];
+      for (int i = 0; i < 4; ++i) v[i] = acc[m][t][q * 4 + i] - za[m] * z[i];
       return v;
     };
     auto scaled = [&](int t, int q) {
@@ -597,7 +619,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
       const i32x4_t v = sums(t, q);
       f32x4_t y;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = i8_scale(v[i], sa, cs[i], cb[i]);
+      for (int i = 0; i < 4; ++i) y[i] = i8_scale(v[i], sa[m], cs[i], cb[i]);
       return y;
     };
     auto out4 = [&](int t, int q) {  // columns 8 q + 4 half .. + 3 of tile t's TC
@@ -618,7 +640,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
 #pragma unroll
       for (int i = lane; i < 32 * per; i += 64) {
         const int row = i / per, piece = i % per;
-        const int y = __shfl(yr, row), j = c0 + piece * (16 / es);
+        const int y = __shfl(yr[m], row), j = c0 + piece * (16 / es);
         const u32x4_t v = *(const u32x4_t*)(strip + row * PITCH + piece * 16);
         if (y < 0 || j >= limit) continue;
         char* dst = (char*)base + ((int64_t)y * ld + j) * es;
