@@ -215,7 +215,7 @@ __global__ __launch_bounds__(256) void gemm_i8_reduce_kernel(const I8Args p, int
 // with random codes, 3.1 with A all zero; 4096 x 14336 x 4096 239-247 us = 2.0
 // POP/s); the small tiles the copies into LDS (16-20 TB/s
 // over the card, so a 64 x 64 tile takes 0.19 us a group where its MFMAs take 0.06);
-// with up to 64 rows HBM (16 x 14336 x 4096 12.3 us = 4.8 TB/s). Row strides
+// with up to 64 rows HBM (16 x 14336 x 4096 11.8 us = 5.0 TB/s). Row strides
 // that are no multiple of 128 bytes split every copied piece over two lines:
 // up to 1.6 times slower in the small tiles. Measured without gain: eight
 // stages instead of four, eight waves sharing the steps of a group, copies of
@@ -829,7 +829,7 @@ hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s) {
 // Expert blocks: the tile holds the block's rows. Two to four workgroups of
 // four waves share a CU, so that one's prologue and epilogue run under the others'
 // loops. Measured (E = 256, top-8; gate+up 4096 x 7168, down 7168 x 2048):
-//   16 rows  32 x 128 tiles half filled (fragments straight from memory: T = 64 down 640 us)
+//   16 rows  32 x 128 tiles half filled (fragments straight from memory: T = 64 down 640 us against 535)
 //   32 rows  32 x 256: T = 512 down 646 us, 32 x 128 720, 32 x 64 759
 //   64 rows  64 x 256, four waves and two stages: T = 4096 gate+up 2.06 ms; eight waves and
 //            four stages (one workgroup a CU) 2.28, 64 x 128 2.35

@@ -11,8 +11,9 @@
 // steps): it names the expert, and equal keys give the lowest index.
 //
 // A choice must not hang on binary32 rounding, yet binary64 scores and 64-bit
-// reductions for all experts take twice the time (8192 tokens x 256 experts
-// in groups: 31 us). So the top_k + 1 largest are taken in binary32 and the
+// reductions for all experts take two and a half times as long (8192 tokens x
+// 256 experts in groups: 31.4 against 11.9 us, bound by some 470 vector
+// instructions a token and the last tokens in doubt). So the top_k + 1 largest are taken in binary32 and the
 // gaps between neighbours are compared with what the keys can be off by. Where
 // a gap does not decide (some 4 % of the tokens of normal logits and biases), four
 // more candidates are taken and ranked by binary64 keys, one lane each; if
