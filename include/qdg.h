@@ -531,7 +531,8 @@ qdg_status qdg_moe_combine_bf16(const void* y, const float* w, int64_t T, int32_
      choice  the top_k experts of the groups that stay with the largest keys,
              in descending order, equal ones the lower index first
      weight  w = s_e of the chosen, with renormalize divided by their sum
-             (0 where the sum is 0), times scale
+             (0 where that is 0: all masked, or all below binary64's
+             smallest value), times scale
    Keys and group values decide as in binary64 (a choice between two that
    binary32 cannot tell apart is not left to its rounding); the weights are
    within 2^-21 of their exact values (relative).

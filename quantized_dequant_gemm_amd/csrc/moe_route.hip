@@ -300,9 +300,9 @@ __device__ __forceinline__ float key_high(uint32_t o, uint32_t index_mask, float
 }
 
 // exp(a - b) for a <= b in binary64 with binary32's relative error 2^-23,
-// 0 below 2^-126.
+// 0 below 2^-126 (where the difference may pass binary32's largest value).
 __device__ __forceinline__ double exp_diff(float a, float b) {
-  const double d = (double)a - (double)b;
+  const double d = fmax((double)a - (double)b, -256.0);
   const float hi = (float)d, lo = (float)(d - (double)hi);
   const float e = expf(hi);
   return (double)__builtin_fmaf(e, lo, e);
@@ -486,10 +486,10 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
     if (BIAS && !(bias[id] > -kInf)) my_x = -kInf;  // masked: weight 0
   }
   double w = 0.0;
-  // renormalised softmax weights need no more than the chosen experts' ratios
-  const float ref = SIGMOID ? 0.f : c.renormalize ? of_order(wave_max(order_of(my_x))) : row.top;
-  const float arg = SIGMOID ? my_x : my_x - ref;
-  if (__ballot(my_x != -kInf && arg < -80.f)) {  // near or past the end of binary32
+  const float ref = SIGMOID ? 0.f : row.top;
+  // scores near or past the end of binary32
+  const bool far = __ballot(my_x != -kInf && my_x - ref < -80.f) != 0;
+  if (far) {
     if (my_x != -kInf) w = SIGMOID ? sigmoid64((double)my_x) : exp((double)my_x - (double)ref);
   } else if (my_x != -kInf) {
     w = SIGMOID ? rcp64(1.0 + (double)expf(-my_x)) : exp_diff(my_x, ref);
@@ -503,7 +503,7 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
     for (int j = 0; j < EPL; ++j) sum += x[j] == -kInf ? 0.0 : exp_diff(x[j], row.top);
     row.sum64 = wave_sum(sum);
   }
-  if (c.renormalize || !SIGMOID) w = row.sum64 > 0.0 ? w * rcp64(row.sum64) : 0.0;
+  if (c.renormalize || !SIGMOID) w = !(row.sum64 > 0.0) ? 0.0 : far ? w / row.sum64 : w * rcp64(row.sum64);
   if (lane < c.top_k) {
     ids[t * c.top_k + lane] = id;
     weights[t * c.top_k + lane] = (float)(w * (double)c.scale);

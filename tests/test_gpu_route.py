@@ -117,6 +117,33 @@ def test_masks_infinities_nan(qdg, score, groups, topk_groups, with_bias, renorm
     check(x, 6, score=score, bias=bias, groups=groups, topk_groups=topk_groups, group_score="max", renorm=renorm)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_logits_far_apart(qdg, score, with_bias, renorm):
+    """Differences past binary32's largest value, and scores past its smallest."""
+    e, big = 48, float(np.finfo(np.float32).max)
+    rng = np.random.default_rng(19)
+    x = 2.0 * rng.standard_normal((8, e))
+    x[0, 3], x[0, 9] = np.inf, -big
+    x[1] = -big
+    x[1, 5] = big
+    x[2, ::2], x[2, 1::2] = 3e38, -3e38
+    x[3] = -700.0 + np.arange(e)
+    x[4] = -90.0 - 0.25 * np.arange(e)
+    x[5] = -3000.0
+    x[5, 7] = -2995.0
+    x[6] = np.linspace(-120.0, 0.0, e)
+    x[7] = np.linspace(80.0, 100.0, e)
+    x = x.astype(np.float32).astype(np.float64)
+    bias = np.where(np.arange(e) % 3 == 0, 1.5, 0.0) if with_bias else None
+    ids, w, _, seen = run(x, 6, score=score, bias=bias, renorm=renorm)
+    rid, rw, _ = ops.route(seen, 6, score=score, bias=bias, renorm=renorm)
+    np.testing.assert_array_equal(ids, rid)
+    # half a step of a subnormal binary32 more where the weight is one
+    assert np.all(np.abs(w - rw) <= 2.0 ** -21 * np.abs(rw) + 2.0 ** -150), (w, rw)
+
+
 @pytest.mark.parametrize("ltype", ["bf16", "f16"])
 def test_lowest_value_of_the_type(qdg, ltype):
     x = np.full((2, 70), float(torch.finfo(DT[ltype][1]).min))
