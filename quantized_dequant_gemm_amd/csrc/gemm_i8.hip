@@ -104,8 +104,8 @@ __device__ __forceinline__ int i8_sum16(u32x4_t v, int acc) {
 // split over the KW waves of a workgroup that owns 16 columns of Y. Bound by
 // the weights' bytes: 16 KiB of loads in flight per CU at once and no barrier
 // in the loop (1 x 4096 x 4096: 5.5 us, 3.3 us of it loop = 5 TB/s; two
-// column tiles per workgroup 7.5 us, the 64 x 64 LDS tiles 9.9 us; from 8192 columns on those
-// are as fast, at 14336 faster: 12.2 against 17 us).
+// column tiles per workgroup 7.5 us, the 64 x 64 LDS tiles 9.9 us; from 8192
+// columns on those are as fast, at 14336 faster: 12.2 against 17 us).
 template <int KW, bool SILU, bool ZP>
 __global__ __launch_bounds__(64 * KW) void gemm_i8_rows_kernel(const I8Args p) {
   constexpr int NT = SILU ? 2 : 1;  // gate and up tile

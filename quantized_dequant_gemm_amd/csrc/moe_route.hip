@@ -13,13 +13,13 @@
 // A choice must not hang on binary32 rounding, yet binary64 scores and 64-bit
 // reductions for all experts take two and a half times as long (8192 tokens x
 // 256 experts in groups: 31.4 against 11.9 us, bound by some 470 vector
-// instructions a token and the last tokens in doubt). So the top_k + 1 largest are taken in binary32 and the
-// gaps between neighbours are compared with what the keys can be off by. Where
-// a gap does not decide (some 4 % of the tokens of normal logits and biases), four
-// more candidates are taken and ranked by binary64 keys, one lane each; if
-// not even these hold the top_k for sure, the whole token is routed in binary64.
-// Without a bias the keys are the logits: exact for 16-bit types, cut by the
-// index bits for binary32 ones.
+// instructions a token and the last tokens in doubt). So the top_k + 1 largest
+// are taken in binary32 and the gaps between neighbours are compared with what
+// the keys can be off by. Where a gap does not decide (some 4 % of the tokens
+// of normal logits and biases), four more candidates are taken and ranked by
+// binary64 keys, one lane each; if not even these hold the top_k for sure, the
+// whole token is routed in binary64. Without a bias the keys are the logits:
+// exact for 16-bit types, cut by the index bits for binary32 ones.
 //
 // Error bounds (with a factor of two or more to spare): exp as v_exp_f32 of
 // x * log2(e) is off by 2^-23 + 1.5 |x| 2^-24 relative. Sigmoid: 1 / (1 + t)
