@@ -395,12 +395,12 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void moe_route_kernel(
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     }
-    float v = c.group_score == QDG_GROUP_MAX || m2 == -kInf ? m1 : m1 + m2;
+    const float v = c.group_score == QDG_GROUP_MAX || m2 == -kInf ? m1 : m1 + m2;
     // two keys' errors and the roundings of keys and sum
     const float err = fabsf(v) < kInf ? 2.f * score_err(SIGMOID) + (fabsf(m1) + (m2 == -kInf ? 0.f : fabsf(m2))) * 0x1p-22f : 0.f;
-    v = __shfl(v, owner & 63);
-    const float dv = __shfl(err, owner & 63);
-    const float vl = v - dv, vu = v + dv;
+    // a sum below binary32's range is no mask: anywhere under its largest magnitude
+    const float vl = __shfl(v - err, owner & 63);
+    const float vu = __shfl(v == -kInf && m1 > -kInf ? -kMax : v + err, owner & 63);
     int maybe = 0;  // groups that may be ahead of this lane's
     for (int g = 0; g < G; ++g) {
       const float ou = readlane_f32(vu, g);

@@ -202,3 +202,25 @@ def test_replayed_graph_and_other_stream(qdg):
         rid, rw, _ = ops.route(y, 8, renorm=True)
         np.testing.assert_array_equal(ids.cpu().numpy(), rid)
         assert np.all(np.abs(w.cpu().numpy() - rw) <= 2.0 ** -21 * rw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("per", [2, 3, 20, 32])
+def test_group_values_past_binary32(qdg, score, per):
+    """Sums of two keys below (or above) binary32's range: finite in binary64, so ahead of a group whose experts are
+    all masked, and in order among themselves."""
+    low, inf = float(np.finfo(np.float32).min), np.inf
+    rng = np.random.default_rng(per)
+    for values in ([-inf, -3e38], [-3.2e38, -2e38], [low, -2.5e38], [-inf, low, -3e38, -inf], [low, low, low, -inf],
+                   [2e38, 3e38], [low, -3e38, -1.8e38, -1e38, 0.0, 1.8e38, 3e38, -inf]):
+        groups = len(values)
+        bias = np.repeat(np.array(values), per)
+        x = rng.standard_normal((5, groups * per))
+        for topk_groups in range(1, groups):
+            check(x, min(per, 4), score=score, bias=bias, groups=groups, topk_groups=topk_groups, group_score="top2")
+    # one finite key of a pair next to a masked one
+    bias = np.full(4 * per, -inf)
+    bias[per:per + 2] = -3e38
+    bias[2 * per] = low
+    check(rng.standard_normal((5, 4 * per)), 1, score=score, bias=bias, groups=4, topk_groups=1, group_score="top2")
+    check(rng.standard_normal((5, 4 * per)), 2, score=score, bias=bias, groups=4, topk_groups=2, group_score="top2")
