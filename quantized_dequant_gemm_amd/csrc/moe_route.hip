@@ -154,7 +154,12 @@ __device__ __forceinline__ void load_row(const void* row, int ltype, bool vec, i
   }
 }
 
-__device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
+// exp of the argument's negative only: exp(-x) passes binary64's range at x <
+// -709.8, where the score is still a number down to 2^-1074.
+__device__ __forceinline__ double sigmoid64(double x) {
+  const double e = exp(-fabs(x));
+  return (x >= 0.0 ? 1.0 : e) / (1.0 + e);
+}
 
 // What the rare binary64 decisions read again: one token's row (cached by
 // then), so that they keep no registers of the common path alive.

@@ -224,3 +224,18 @@ def test_group_values_past_binary32(qdg, score, per):
     bias[2 * per] = low
     check(rng.standard_normal((5, 4 * per)), 1, score=score, bias=bias, groups=4, topk_groups=1, group_score="top2")
     check(rng.standard_normal((5, 4 * per)), 2, score=score, bias=bias, groups=4, topk_groups=2, group_score="top2")
+
+
+@pytest.mark.parametrize("groups", [1, 4])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_sigmoid_scores_below_the_smallest_normal(qdg, groups, group_score):
+    """sigmoid(-725) = 2^-1046 is a binary64 number (a subnormal one with 28 bits): scores there have an order, group
+    values and renormalised weights (28 bits in, one step of exp and half steps of sum and quotient: far below 2^-21)."""
+    e = 32
+    x = np.empty((3, e))
+    x[0] = -725.0 + 0.25 * np.arange(e)
+    x[1] = -711.0 - 0.25 * np.arange(e)
+    x[2] = -718.0
+    check(x, 6, score="sigmoid", groups=groups, topk_groups=max(1, groups // 2), group_score=group_score, renorm=True)
+    check(x, 6, score="sigmoid", bias=np.zeros(e), groups=groups, topk_groups=max(1, groups // 2),
+          group_score=group_score, renorm=True)
