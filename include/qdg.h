@@ -563,7 +563,7 @@ typedef struct qdg_route_config {
    enqueues nothing). Device pointers aligned to their elements. One launch,
    no workspace. Errors: QDG_ERR_INVALID_ARG (NULL pointers, T < 0, a config
    value out of its range), QDG_ERR_UNSUPPORTED (more than 1024 experts, 64
-   groups or top_k 32, T > 2^26), QDG_ERR_MISALIGNED. */
+   groups or top_k 32, T > 2^26 - 4), QDG_ERR_MISALIGNED. */
 qdg_status qdg_moe_route(const qdg_route_config* cfg, const void* logits, int64_t ld, const float* bias, int64_t T,
                          int32_t* topk_ids, float* topk_weights, uint32_t* status, void* stream);
 

@@ -38,7 +38,8 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
 constexpr int64_t kMaxStride = (int64_t)1 << 28;  // eight rows within 32-bit offsets
-constexpr int64_t kMaxSide = (int64_t)1 << 26;  // tokens routed, rows and columns of the int8 products: launches stay within 2^32 threads
+constexpr int64_t kMaxSide = (int64_t)1 << 26;  // rows and columns of the int8 products
+constexpr int64_t kMaxTokens = ((int64_t)1 << 26) - 4;  // routed: one wave each, a launch holds fewer than 2^32 threads
 
 // The checks that the dense and the grouped product share.
 qdg_status check_i8(const qdg_i8_config* c) {
@@ -118,7 +119,7 @@ qdg_status qdg_moe_route(const qdg_route_config* cfg, const void* logits, int64_
   if (c.num_experts > 1024) return fail(QDG_ERR_UNSUPPORTED, "at most 1024 experts");
   if (c.top_k > 32) return fail(QDG_ERR_UNSUPPORTED, "top_k must be at most 32");
   if (c.num_groups > 64) return fail(QDG_ERR_UNSUPPORTED, "at most 64 groups");
-  if (T > kMaxSide) return fail(QDG_ERR_UNSUPPORTED, "T must be at most 2^26");
+  if (T > kMaxTokens) return fail(QDG_ERR_UNSUPPORTED, "T must be at most 2^26 - 4");
   if (c.ltype != QDG_L_BF16 && c.ltype != QDG_L_F16 && c.ltype != QDG_L_F32)
     return fail(QDG_ERR_INVALID_ARG, "ltype must be BF16, F16 or F32");
   if (c.score != QDG_SCORE_SOFTMAX && c.score != QDG_SCORE_SIGMOID) return fail(QDG_ERR_INVALID_ARG, "bad score");

@@ -130,3 +130,9 @@ def test_messages_name_the_cause():
         q.qdg_moe_route(q.route(64, 4, num_groups=3), P, 64, None, 1, P, P)
     with pytest.raises(q.QdgError, match="multiples of 16"):
         q.qdg_gemm_i8(q.gemm_i8(64, 64, lda=72), P, P, None, P, P, None, P, 1)
+
+
+def test_route_refuses_what_one_launch_cannot_hold():
+    """Four tokens a block of 256 threads, below 2^32 threads: 2^26 - 4 tokens are the most."""
+    for t in ((1 << 26) - 3, 1 << 26, (1 << 26) + 1):
+        assert _route(T=t) == q.QDG_ERR_UNSUPPORTED

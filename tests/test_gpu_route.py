@@ -239,3 +239,17 @@ def test_sigmoid_scores_below_the_smallest_normal(qdg, groups, group_score):
     check(x, 6, score="sigmoid", groups=groups, topk_groups=max(1, groups // 2), group_score=group_score, renorm=True)
     check(x, 6, score="sigmoid", bias=np.zeros(e), groups=groups, topk_groups=max(1, groups // 2),
           group_score=group_score, renorm=True)
+
+
+def test_largest_number_of_tokens(qdg):
+    t = (1 << 26) - 4
+    x = torch.zeros(t, dtype=torch.float16, device="cuda")
+    x[-1] = 3.0
+    ids = torch.full((t + 1,), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((t + 1,), -7.0, dtype=torch.float32, device="cuda")
+    cfg = q.route(1, 1, ltype=q.QDG_L_F16, score=q.QDG_SCORE_SIGMOID)
+    q.qdg_moe_route(cfg, x.data_ptr(), 1, None, t, ids.data_ptr(), w.data_ptr(), q.current_stream())
+    torch.cuda.synchronize()
+    assert int(ids[:t].abs().max()) == 0 and bool((w[:t - 1] == 0.5).all())
+    assert abs(float(w[t - 1]) - 1 / (1 + np.exp(-3.0))) < 2.0 ** -21
+    assert int(ids[t]) == -7 and float(w[t]) == -7.0
