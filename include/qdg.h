@@ -607,10 +607,12 @@ typedef struct qdg_i8_config {
   int32_t num_experts, otype, epilogue, reserved; /* reserved: 0 */
 } qdg_i8_config;
 
-/* Workspace bytes qdg_gemm_i8 needs for M rows (0: none; int32 partials of a
-   product whose K is split over workgroups, added by a second kernel). Its
-   contents need no initialisation. Calls that share a workspace must be
-   ordered on one stream. */
+/* Workspace bytes that serve qdg_gemm_i8 for M rows and for any fewer (0:
+   none; int32 partials of a product whose K is split over workgroups, added
+   by a second kernel). Fewer rows may be split where many are not, so the
+   call looks at all of them: ask once, for the largest batch. The contents
+   need no initialisation. Calls that share a workspace must be ordered on
+   one stream. */
 qdg_status qdg_gemm_i8_workspace(const qdg_i8_config* cfg, int64_t M, size_t* bytes);
 
 /* Y[m][j] = a_scales[m] * b_scales[j] * sum_k (A[m][k] - a_zeros[m]) * B[j][k]

@@ -97,9 +97,14 @@ qdg_status i8_args(const qdg_i8_config* c, const int8_t* A, const float* a_scale
   return QDG_OK;
 }
 
-size_t i8_workspace(const qdg_i8_config* c, int64_t M) {
+int64_t i8_vcols(const qdg_i8_config* c) {
   const bool silu = c->epilogue == QDG_EPI_SILU_MUL;
-  const int64_t vcols = gemm_i8_vcols(silu ? c->n / 2 : c->n, silu);
+  return gemm_i8_vcols(silu ? c->n / 2 : c->n, silu);
+}
+
+// Bytes of the partials of a product of M rows.
+size_t i8_workspace(const qdg_i8_config* c, int64_t M) {
+  const int64_t vcols = i8_vcols(c);
   const int split = M > 0 ? gemm_i8_split(M, vcols, c->k) : 1;
   return split > 1 ? (size_t)split * (size_t)M * (size_t)vcols * sizeof(int32_t) : 0;
 }
@@ -165,7 +170,7 @@ qdg_status qdg_gemm_i8_workspace(const qdg_i8_config* cfg, int64_t M, size_t* by
   if (cfg->num_experts != 1) return fail(QDG_ERR_INVALID_ARG, "the dense product has one expert");
   if (M < 0) return fail(QDG_ERR_INVALID_ARG, "M < 0");
   if (M > kMaxSide) return fail(QDG_ERR_UNSUPPORTED, "M must be at most 2^26");
-  *bytes = i8_workspace(cfg, M);
+  *bytes = (size_t)gemm_i8_max_partial_rows(M, i8_vcols(cfg), cfg->k) * (size_t)i8_vcols(cfg) * sizeof(int32_t);
   return QDG_OK;
 }
 

@@ -7,6 +7,9 @@
 // consecutive columns of one row of Y. With the SiLU*mul epilogue the 16-column tiles
 // of B alternate between gate and up rows, so that a lane holds both halves.
 
+#include <algorithm>
+#include <iterator>
+
 #include "qdg_device.h"
 #include "qdg_internal.h"
 
@@ -796,6 +799,29 @@ hipError_t launch_dense_tile(I8Kernel kernel, const I8Args& a, bool silu, int sp
 int64_t gemm_i8_vcols(int64_t cols, bool silu) { return (cols + 15) / 16 * 16 * (silu ? 2 : 1); }
 
 int gemm_i8_split(int64_t M, int64_t vcols, int64_t k) { return choose_dense(M, vcols, k).split; }
+
+// Within 64 rows every tile's counts stay as they are, and a choice's time
+// grows with its split times the rows: the split taken never grows there, so
+// that equal splits at both ends are the split of all rows between.
+int64_t gemm_i8_max_partial_rows(int64_t M, int64_t vcols, int64_t k) {
+  // two parts of eight groups at least, and of the largest tiles, must fit one round
+  const I8Tile& large = kI8Tiles[std::size(kI8Tiles) - 1];
+  const int64_t limit = k > 15 * 128 ? kCus / 2 / ((vcols + large.bn - 1) / large.bn) * large.bm : 0;
+  auto rows_of = [&](int64_t m) {
+    const int64_t split = gemm_i8_split(m, vcols, k);
+    return split > 1 ? split * m : 0;
+  };
+  int64_t most = 0;
+  for (int64_t lo = 1, hi; lo <= std::min(M, limit); lo = hi + 1) {
+    hi = std::min({(lo + 63) / 64 * 64, M, limit});
+    if (lo <= 16 && hi > 16) hi = 16;  // up to here perhaps the rows kernel
+    most = std::max(most, rows_of(hi));
+    const int at_end = gemm_i8_split(hi, vcols, k);
+    if (gemm_i8_split(lo, vcols, k) == at_end) continue;
+    for (int64_t m = lo; m < hi && gemm_i8_split(m, vcols, k) != at_end; ++m) most = std::max(most, rows_of(m));
+  }
+  return most;
+}
 
 hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s) {
   const I8Choice c = choose_dense(a.M, a.vcols, a.k);

@@ -188,6 +188,8 @@ struct I8Args {
 constexpr uint32_t kI8FarRow = 0xF0000000u;
 int64_t gemm_i8_vcols(int64_t cols, bool silu);
 int gemm_i8_split(int64_t M, int64_t vcols, int64_t k);
+// the largest split * M' (0: no split) over M' <= M
+int64_t gemm_i8_max_partial_rows(int64_t M, int64_t vcols, int64_t k);
 hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s);
 hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int m_blocks, hipStream_t s);
 

@@ -136,3 +136,22 @@ def test_route_refuses_what_one_launch_cannot_hold():
     """Four tokens a block of 256 threads, below 2^32 threads: 2^26 - 4 tokens are the most."""
     for t in ((1 << 26) - 3, 1 << 26, (1 << 26) + 1):
         assert _route(T=t) == q.QDG_ERR_UNSUPPORTED
+
+
+def test_workspace_of_the_largest_batch_serves_smaller_ones():
+    """Fewer rows may be split where many are not: the bytes never fall with M."""
+    for n, k, epi in ((4096, 14336, 0), (4096, 4096, 0), (576, 7168, 0), (130, 65536, 1), (9002, 40001, 0), (28672, 8192, 1)):
+        cfg = q.gemm_i8(n, k, epilogue=epi)
+        need = [q.qdg_gemm_i8_workspace(cfg, m) for m in list(range(0, 700)) + [4096, 32769, 1 << 26]]
+        assert need == sorted(need), (n, k)
+    cfg = q.gemm_i8(4096, 14336)
+    assert q.qdg_gemm_i8_workspace(cfg, 4096) >= q.qdg_gemm_i8_workspace(cfg, 64) > 0
+    assert q.qdg_gemm_i8_workspace(q.gemm_i8(4096, 1920), 1 << 26) == 0  # no K that is ever split
+    assert q.qdg_gemm_i8_workspace(q.gemm_i8(33000, 65536), 1 << 26) == 0  # nor so many columns
+    # a split product is refused a workspace that is too small or misaligned, others need none
+    for M, n, k in ((33, 514, 16386), (64, 128, 8192), (300, 128, 65536)):
+        need = q.qdg_gemm_i8_workspace(q.gemm_i8(n, k), M)
+        assert need > 0
+        assert _gemm(M=M, n=n, k=k, ws_bytes=need - 1) == q.QDG_ERR_WORKSPACE
+        assert _gemm(M=M, n=n, k=k, ws=None) == q.QDG_ERR_WORKSPACE
+        assert _gemm(M=M, n=n, k=k, ws=P + 8) == q.QDG_ERR_MISALIGNED

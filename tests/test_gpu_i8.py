@@ -497,3 +497,21 @@ def test_two_streams_with_their_own_workspaces(qdg):
     torch.cuda.synchronize()
     for y in ys:
         assert torch.equal(y, want)
+
+
+def test_one_workspace_for_every_batch(qdg):
+    """The bytes asked for the largest batch, which is not split itself, serve the smaller ones that are."""
+    n, k, rows = 2050, 16400, 600
+    L = Layer(np.random.default_rng(51), rows, n, k, zeros=True, bias=False)
+    cfg = L.cfg(q.QDG_O_I32, q.QDG_EPI_NONE)
+    nbytes = q.qdg_gemm_i8_workspace(cfg, rows)
+    assert nbytes > 0
+    ws = torch.full((nbytes + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    want = ops.int_product(L.a, L.b[0], L.za)
+    for M in (1, 17, 33, 64, 65, 128, 129, 300, 600):
+        y = torch.full((M + 1, n), 77, dtype=torch.int32, device="cuda")
+        q.qdg_gemm_i8(cfg, L.dA.data_ptr(), L.dsa.data_ptr(), L.dza.data_ptr(), L.dB.data_ptr(), L.dsb.data_ptr(),
+                      None, y.data_ptr(), M, ws.data_ptr(), nbytes, q.current_stream())
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(y[:M].cpu().numpy(), want[:M])
+        assert (y[M] == 77).all() and (ws[nbytes:] == 0x5A).all()
