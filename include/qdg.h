@@ -615,6 +615,14 @@ typedef struct qdg_i8_config {
    one stream. */
 qdg_status qdg_gemm_i8_workspace(const qdg_i8_config* cfg, int64_t M, size_t* bytes);
 
+/* Writes a one-line record of what qdg_gemm_i8 runs for M rows into buf:
+   family (rows: up to 16 rows straight from memory; tile), tile sizes and K
+   split of the first `columns` columns of B in the kernel's order (rounded up
+   to 16; with QDG_EPI_SILU_MUL gate and up alternate by 16), and the tile of
+   those behind them (rest). Host only. Returns the length of the full record
+   (snprintf semantics), -1 on error. */
+int qdg_gemm_i8_describe(const qdg_i8_config* cfg, int64_t M, char* buf, size_t len);
+
 /* Y[m][j] = a_scales[m] * b_scales[j] * sum_k (A[m][k] - a_zeros[m]) * B[j][k]
    + bias[j], the sum exact in int32, then the epilogue and one rounding to
    otype. cfg->num_experts = 1. a_scales f32 [M]; a_zeros i32 [M], values in

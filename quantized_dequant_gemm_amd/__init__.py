@@ -40,7 +40,7 @@ EXPORTS = (
     "qdg_plan_describe", "qdg_moe_describe", "qdg_gemm", "qdg_moe_align_capacity", "qdg_moe_align",
     "qdg_moe_gemm", "qdg_moe_combine", "qdg_moe_combine_bf16", "qdg_plan_autotune", "qdg_plan_autotune_reset",
     "qdg_plan_jit", "qdg_gemm_noalloc", "qdg_moe_route", "qdg_quantize_act_zp", "qdg_gemm_i8_workspace",
-    "qdg_gemm_i8", "qdg_moe_gemm_i8",
+    "qdg_gemm_i8_describe", "qdg_gemm_i8", "qdg_moe_gemm_i8",
 )
 
 
@@ -123,6 +123,7 @@ def load():
         "qdg_moe_route": (I32, [P, P, I64, P, I64, P, P, P, P]),
         "qdg_quantize_act_zp": (I32, [P, I64, I64, I64, P, I64, P, P, P]),
         "qdg_gemm_i8_workspace": (I32, [P, I64, P]),
+        "qdg_gemm_i8_describe": (ctypes.c_int, [P, I64, ctypes.c_char_p, SZ]),
         "qdg_gemm_i8": (I32, [P, P, P, P, P, P, P, P, I64, P, SZ, P]),
         "qdg_moe_gemm_i8": (I32, [P, P, P, P, P, P, P, P, P, P, I64, I32, I32, I32, P, P]),
     }
@@ -311,6 +312,15 @@ def qdg_gemm_i8_workspace(cfg, M):
     out = ctypes.c_size_t()
     _check(load().qdg_gemm_i8_workspace(ctypes.byref(cfg), M, ctypes.byref(out)))
     return out.value
+
+
+def qdg_gemm_i8_describe(cfg, M):
+    n = load().qdg_gemm_i8_describe(ctypes.byref(cfg), M, None, 0)
+    if n < 0:
+        raise QdgError(QDG_ERR_INVALID_ARG, "describe failed")
+    buf = ctypes.create_string_buffer(n + 1)
+    load().qdg_gemm_i8_describe(ctypes.byref(cfg), M, buf, n + 1)
+    return buf.value.decode()
 
 
 def qdg_gemm_i8(cfg, A, a_scales, a_zeros, B, b_scales, bias, Y, M, workspace=None, ws_bytes=0, stream=0):

@@ -174,6 +174,19 @@ qdg_status qdg_gemm_i8_workspace(const qdg_i8_config* cfg, int64_t M, size_t* by
   return QDG_OK;
 }
 
+int qdg_gemm_i8_describe(const qdg_i8_config* cfg, int64_t M, char* buf, size_t len) {
+  if (check_i8(cfg) != QDG_OK || cfg->num_experts != 1 || M < 0 || M > kMaxSide) return -1;
+  const I8Instance i = gemm_i8_instance(M > 0 ? M : 1, i8_vcols(cfg), cfg->k);
+  char rest[48] = "none";
+  if (i.rest_m) snprintf(rest, sizeof rest, "%dx%d", i.rest_m, i.rest_n);
+  return snprintf(buf, buf ? len : 0,
+                  "gemm-i8 dense n=%lld k=%lld M=%lld: family=%s block_m=%d block_n=%d split_k=%d columns=%lld rest=%s "
+                  "epilogue=%s arch=gfx950",
+                  (long long)cfg->n, (long long)cfg->k, (long long)M, i.block_m == 16 ? "rows" : "tile", i.block_m,
+                  i.block_n, i.split, (long long)i.columns, rest,
+                  cfg->epilogue == QDG_EPI_SILU_MUL ? "silu_mul" : "none");
+}
+
 qdg_status qdg_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const float* a_scales, const int32_t* a_zeros,
                        const int8_t* B, const float* b_scales, const float* bias, void* Y, int64_t M,
                        void* workspace, size_t ws_bytes, void* stream) {

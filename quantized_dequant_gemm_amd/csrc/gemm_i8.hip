@@ -823,6 +823,23 @@ int64_t gemm_i8_max_partial_rows(int64_t M, int64_t vcols, int64_t k) {
   return most;
 }
 
+I8Instance gemm_i8_instance(int64_t M, int64_t vcols, int64_t k) {
+  const I8Choice c = choose_dense(M, vcols, k);
+  I8Instance r = {16, 16, c.split, vcols, 0, 0};  // the rows kernel: 16 columns a workgroup
+  for (const I8Tile& t : kI8Tiles) {
+    if (t.kernel == c.kernel) {
+      r.block_m = t.bm;
+      r.block_n = t.bn;
+      if (c.n_main > 0) r.columns = (int64_t)c.n_main * t.bn;
+    }
+    if (c.n_main > 0 && t.kernel == c.rest) {
+      r.rest_m = t.bm;
+      r.rest_n = t.bn;
+    }
+  }
+  return r;
+}
+
 hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s) {
   const I8Choice c = choose_dense(a.M, a.vcols, a.k);
   if (c.kernel == I8_ROWS) {

@@ -190,6 +190,15 @@ int64_t gemm_i8_vcols(int64_t cols, bool silu);
 int gemm_i8_split(int64_t M, int64_t vcols, int64_t k);
 // the largest split * M' (0: no split) over M' <= M
 int64_t gemm_i8_max_partial_rows(int64_t M, int64_t vcols, int64_t k);
+// What runs a dense product: tiles of block_m x block_n (16 x 16: the rows
+// kernel), K in `split` parts, for the first `columns` of B's tile order; the
+// columns behind them in rest_m x rest_n (0: there are none).
+struct I8Instance {
+  int block_m, block_n, split;
+  int64_t columns;
+  int rest_m, rest_n;
+};
+I8Instance gemm_i8_instance(int64_t M, int64_t vcols, int64_t k);
 hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s);
 hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int m_blocks, hipStream_t s);
 

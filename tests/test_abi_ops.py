@@ -155,3 +155,19 @@ def test_workspace_of_the_largest_batch_serves_smaller_ones():
         assert _gemm(M=M, n=n, k=k, ws_bytes=need - 1) == q.QDG_ERR_WORKSPACE
         assert _gemm(M=M, n=n, k=k, ws=None) == q.QDG_ERR_WORKSPACE
         assert _gemm(M=M, n=n, k=k, ws=P + 8) == q.QDG_ERR_MISALIGNED
+
+
+def test_gemm_describe():
+    record = q.qdg_gemm_i8_describe(q.gemm_i8(4096, 4096), 16)
+    assert record == ("gemm-i8 dense n=4096 k=4096 M=16: family=rows block_m=16 block_n=16 split_k=1 columns=4096 "
+                      "rest=none epilogue=none arch=gfx950")
+    record = q.qdg_gemm_i8_describe(q.gemm_i8(4610, 900, epilogue=q.QDG_EPI_SILU_MUL), 4096)
+    assert "family=tile block_m=256 block_n=256 split_k=1 columns=4096 rest=128x128 epilogue=silu_mul" in record
+    assert "split_k=8" in q.qdg_gemm_i8_describe(q.gemm_i8(514, 16386), 33)
+    assert q.qdg_gemm_i8_describe(q.gemm_i8(64, 64), 0).startswith("gemm-i8 dense n=64 k=64 M=0: ")
+    describe = q.load().qdg_gemm_i8_describe
+    assert describe(None, 1, None, 0) == -1
+    for cfg, M in ((q.gemm_i8(0, 64), 1), (q.gemm_i8(64, 64, num_experts=2), 1), (q.gemm_i8(64, 64), -1),
+                   (q.gemm_i8(64, 64), (1 << 26) + 1)):
+        with pytest.raises(q.QdgError):
+            q.qdg_gemm_i8_describe(cfg, M)
