@@ -120,3 +120,26 @@ def test_rows_do_not_depend_on_the_tile(qdg, otype, epi, zeros):
         for first in (0, 4097 - m):
             assert torch.equal(o.call(m, otype, epi, zeros, True, first=first), full[first:first + m]), (m, first)
     assert {"rows", "64x64", "128x64", "128x128", "128x256", "256x256"} <= seen
+
+
+def test_two_streams_with_a_split_each(qdg):
+    """Two split products with inputs and a workspace of their own, on two streams at once."""
+    n, k = 514, 16386
+    runs = []
+    for i, M in enumerate((33, 40)):
+        o = Operands(60 + i, M, n, k)
+        cfg = o.cfg(q.QDG_O_F32, NONE)
+        need = q.qdg_gemm_i8_workspace(cfg, M)
+        assert need > 0 and _kernel(_record(M, n, k)) == "64x64/8"
+        want = o.call(M, q.QDG_O_F32, NONE, True, True)
+        runs.append((o, cfg, need, want, torch.empty(need, dtype=torch.uint8, device="cuda"),
+                     torch.zeros((8, M, n), device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(8):
+        for o, cfg, need, want, ws, ys, st in runs:
+            q.qdg_gemm_i8(cfg, o.A.data_ptr(), o.sa.data_ptr(), o.za.data_ptr(), o.B.data_ptr(), o.sb.data_ptr(),
+                          o.bias.data_ptr(), ys[i].data_ptr(), o.M, ws.data_ptr(), need, st.cuda_stream)
+    torch.cuda.synchronize()
+    for o, cfg, need, want, ws, ys, st in runs:
+        for i in range(8):
+            assert torch.equal(ys[i], want)
