@@ -147,9 +147,11 @@ def _ref(x):
 def current_stream():
     """The handle of torch's current stream on its current device. Read without
     building a torch.cuda.Stream, which takes 3 us of host time: as long as
-    launching a small kernel does."""
+    launching a small kernel does. The raw handle is no public part of torch:
+    where it is missing, the stream object gives the same one."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
 
 
 # ------------------------------------------------------------- entry points

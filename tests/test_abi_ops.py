@@ -171,3 +171,17 @@ def test_gemm_describe():
                    (q.gemm_i8(64, 64), (1 << 26) + 1)):
         with pytest.raises(q.QdgError):
             q.qdg_gemm_i8_describe(cfg, M)
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_current_stream_handle(monkeypatch, raw):
+    """The handle of the current device's current stream, from torch's raw handle where that exists."""
+    import types
+
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=1000 + torch.cuda.current_device()))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
+    if not raw:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert q.current_stream() == 1003
