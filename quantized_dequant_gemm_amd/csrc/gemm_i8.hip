@@ -2,7 +2,8 @@
 //
 //   Y[m][j] = sa[m] * sb[j] * (sum_k A[m][k] B[j][k] - za[m] * sum_k B[j][k]) + bias[j]
 //
-// with both sums exact in int32 on v_mfma_i32_16x16x64_i8 and dot products.
+// with both sums exact in int32 on int8 MFMAs (16 x 16 x 64 in the rows kernel,
+// 32 x 32 x 32 in the tiles) and dot products.
 // The weights are the MFMA's row operand, so a lane of the result holds four
 // consecutive columns of one row of Y. With the SiLU*mul epilogue the 16-column tiles
 // of B alternate between gate and up rows, so that a lane holds both halves.
@@ -103,15 +104,17 @@ __device__ __forceinline__ int i8_sum16(u32x4_t v, int acc) {
   return acc;
 }
 
+constexpr int kRowWaves = 8;
+
 // Up to 16 rows and few columns: fragments straight from memory, the K range
-// split over the KW waves of a workgroup that owns 16 columns of Y. Bound by
+// split over the eight waves of a workgroup that owns 16 columns of Y. Bound by
 // the weights' bytes: 16 KiB of loads in flight per CU at once and no barrier
 // in the loop (1 x 4096 x 4096: 5.5 us, 3.3 us of it loop = 5 TB/s; two
 // column tiles per workgroup 7.5 us, the 64 x 64 LDS tiles 9.9 us; from 8192
 // columns on those are as fast, at 14336 faster: 12.2 against 17 us).
-template <int KW, bool SILU, bool ZP>
-__global__ __launch_bounds__(64 * KW) void gemm_i8_rows_kernel(const I8Args p) {
-  constexpr int NT = SILU ? 2 : 1;  // gate and up tile
+template <bool SILU, bool ZP>
+__global__ __launch_bounds__(64 * kRowWaves) void gemm_i8_rows_kernel(const I8Args p) {
+  constexpr int KW = kRowWaves, NT = SILU ? 2 : 1;  // gate and up tile
   __shared__ i32x4_t red[KW][NT][64];
   __shared__ int zred[KW][NT][16];
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
@@ -260,7 +263,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t i8_rows_rsrc(const int8_t* bas
 }
 
 // Copies FROM .. TO - 1 of group g into one stage (every wave issues the same
-// number). Buffer loads, because the compiler tracks them apart from LDS
+// number). TAG, here and below, is not used: it gives every calling function
+// its own specialization (hipcc's host pass rejects a second function that
+// calls the same specialization of a device function using target builtins). Buffer loads, because the compiler tracks them apart from LDS
 // reads; a global load to LDS in flight makes it wait for every LDS read
 // where one would do.
 template <int FROM, int TO, int LOADS, int NW, int TAG>
@@ -401,7 +406,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   constexpr int LOADS = (BM + BN) / 8 / NW, TAG = ((WM * 8 + WN) * 8 + TM) * 512 + (TN * 8 + NS) * 8 + SILU * 4 + ZP * 2 + MOE;
   static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0, "every wave issues the same copies of A and of B");
   constexpr int A_LOADS = BM / 8 / NW;
-  static_assert(NS >= 2 && NS <= 8 && NS * BYTES <= 160 * 1024, "two to eight stages within LDS");
+  static_assert(NS >= 2 && NS <= 4 && NS * BYTES <= 160 * 1024, "two to four stages within LDS");
   static_assert(LOADS * (NS - 1) < 64, "vmcnt holds the copies in flight");
   // separate objects, so that the compiler can tell a copy into one stage
   // from a read of another
@@ -409,11 +414,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(const I8Args
   __shared__ __attribute__((aligned(1024))) char st1[BYTES];
   __shared__ __attribute__((aligned(1024))) char st2[NS > 2 ? BYTES : 16];
   __shared__ __attribute__((aligned(1024))) char st3[NS > 3 ? BYTES : 16];
-  __shared__ __attribute__((aligned(1024))) char st4[NS > 4 ? BYTES : 16];
-  __shared__ __attribute__((aligned(1024))) char st5[NS > 5 ? BYTES : 16];
-  __shared__ __attribute__((aligned(1024))) char st6[NS > 6 ? BYTES : 16];
-  __shared__ __attribute__((aligned(1024))) char st7[NS > 7 ? BYTES : 16];
-  char* const stage[8] = {st0, st1, st2, st3, st4, st5, st6, st7};
+  char* const stage[4] = {st0, st1, st2, st3};
   const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -845,11 +846,11 @@ hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s) {
   if (c.kernel == I8_ROWS) {
     const dim3 grid((unsigned)((a.cols + 15) / 16));
     auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, dim3(512), 0, s, a);
+      hipLaunchKernelGGL(kernel, grid, dim3(64 * kRowWaves), 0, s, a);
       return hipGetLastError();
     };
-    if (silu) return a.a_zeros ? go(gemm_i8_rows_kernel<8, true, true>) : go(gemm_i8_rows_kernel<8, true, false>);
-    return a.a_zeros ? go(gemm_i8_rows_kernel<8, false, true>) : go(gemm_i8_rows_kernel<8, false, false>);
+    if (silu) return a.a_zeros ? go(gemm_i8_rows_kernel<true, true>) : go(gemm_i8_rows_kernel<true, false>);
+    return a.a_zeros ? go(gemm_i8_rows_kernel<false, true>) : go(gemm_i8_rows_kernel<false, false>);
   }
   hipError_t e = launch_dense_tile(c.kernel, a, silu, c.split, s, c.n_main);
   if (e != hipSuccess) return e;
