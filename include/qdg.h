@@ -195,9 +195,9 @@ typedef struct qdg_std_weights {
 
 typedef struct qdg_plan qdg_plan;
 
-/* Input flags: bits that qdg_preprocess, qdg_moe_align and
-   qdg_moe_route OR into an optional caller-owned device status word (uint32_t, 4-byte aligned) when
-   they meet input the standard format does not allow. The call still
+/* Input flags: bits that qdg_preprocess, qdg_moe_align and qdg_moe_route OR
+   into an optional caller-owned device status word (uint32_t, 4-byte
+   aligned) when they meet input the standard format does not allow. The call still
    completes and its outputs are defined (noted per flag); a caller that
    passes the word zeroes it beforehand and reads it after the stream has
    run. The library never clears it, so one word can collect the flags of
@@ -535,7 +535,8 @@ qdg_status qdg_moe_combine_bf16(const void* y, const float* w, int64_t T, int32_
              smallest value), times scale
    Keys and group values decide as in binary64 (a choice between two that
    binary32 cannot tell apart is not left to its rounding); the weights are
-   within 2^-21 of their exact values (relative).
+   within 2^-21 of their exact values (relative; a subnormal one within half
+   a step of binary32).
    Masked experts: a logit of -infinity or NaN, or a bias of -infinity or
    NaN, masks an expert: its score is 0, it ranks behind every expert that
    is not masked and adds nothing to a group's value (a group of masked
@@ -570,9 +571,12 @@ qdg_status qdg_moe_route(const qdg_route_config* cfg, const void* logits, int64_
 /* ------------------------------------- int8 products over stored operands
    The W8A8 product over row-major operands as they are stored: no
    qdg_preprocess, any n and k, row strides, a zero point for each token, a
-   bias, and the SiLU*mul epilogue for dense layers too. For weights that
-   change between calls, for operands that are views, and for activations
-   that lie on one side of zero (asymmetric codes spend all 256 on them).
+   bias, and the SiLU*mul epilogue for dense layers too. Activations that lie
+   on one side of zero spend all 256 codes; weights may change between calls
+   and operands may be views. Dense, it is also the faster W8A8 product from
+   some 17 rows on (K = 4096, n = 4096: 64 rows 13 us against 17 over packed
+   weights, 4096 rows 65 against 88); up to 16 rows qdg_gemm over packed
+   weights takes as long or up to an eighth less.
 
    Asymmetric activation quantizer: per token, over the finite values of its
    row, lo = min(0, min x), hi = max(0, max x);
@@ -593,8 +597,7 @@ qdg_status qdg_quantize_act_zp(const void* a_bf16, int64_t lda, int64_t M, int64
 
 /* A layer of the direct int8 product. B i8 [num_experts][n][k], rows of ldb
    bytes, experts n * ldb bytes apart; lda and ldb multiples of 16 (fastest: of
-   128), >= k, <= 2^28; Y
-   rows of ldy elements, >= its columns (n, or n / 2 with QDG_EPI_SILU_MUL).
+   128), >= k, <= 2^28; Y rows of ldy elements, >= its columns (n, or n / 2 with QDG_EPI_SILU_MUL).
    otype BF16, F32, or I32 (the exact integers; scales and bias are ignored
    and may be NULL; not with an epilogue). epilogue QDG_EPI_NONE or
    QDG_EPI_SILU_MUL (n even: rows [0, n/2) of B the gate, [n/2, n) the up
@@ -624,14 +627,19 @@ qdg_status qdg_gemm_i8_workspace(const qdg_i8_config* cfg, int64_t M, size_t* by
 int qdg_gemm_i8_describe(const qdg_i8_config* cfg, int64_t M, char* buf, size_t len);
 
 /* Y[m][j] = a_scales[m] * b_scales[j] * sum_k (A[m][k] - a_zeros[m]) * B[j][k]
-   + bias[j], the sum exact in int32, then the epilogue and one rounding to
-   otype. cfg->num_experts = 1. a_scales f32 [M]; a_zeros i32 [M], values in
+   + bias[j], then the epilogue. The sum is exact in int32; behind it come
+   binary32 operations: f32(sum) * a_scale, times b_scale plus bias in one
+   fused step (three roundings of 2^-24 before the one to otype; each value
+   within binary32's range), and with SILU_MUL g / (1 + exp(-g)) * u, whose
+   gate below -88.7 counts as 0 (exactly: at most 2^-121).
+   cfg->num_experts = 1. a_scales f32 [M]; a_zeros i32 [M], values in
    [-128, 127], or NULL (all 0); b_scales f32 [n]; bias f32 [n] or NULL. A and
    B 16-byte aligned, the others aligned to their elements; workspace 16-byte
    aligned, NULL where none is needed. Bytes of A and B rows behind k may hold
    anything. M in [0, 2^26] (0 enqueues nothing). QDG_ERR_UNSUPPORTED also
-   where Y has more tiles than one launch holds (at least 2^28 elements). Row m of Y does not depend
-   on M or on the other rows, and results are the same on every call. */
+   where Y has more tiles than one launch holds (at least 2^28 elements). Row m
+   of Y does not depend on M or on the other rows, and results are the same on
+   every call. */
 qdg_status qdg_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const float* a_scales, const int32_t* a_zeros,
                        const int8_t* B, const float* b_scales, const float* bias, void* Y, int64_t M,
                        void* workspace, size_t ws_bytes, void* stream);

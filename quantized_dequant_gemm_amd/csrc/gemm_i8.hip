@@ -26,10 +26,14 @@ __device__ __forceinline__ void i8_tile(const I8Args& p, int vt, int& first, int
 }
 
 // One form in every kernel, so that a row does not depend on which one ran.
+// In binary32, as the outputs are at most: three roundings of half a step
+// (2^-24) behind the exact sum, far below bf16's 2^-8.
 __device__ __forceinline__ float i8_scale(int acc, float sa, float sb, float bias) {
   return __builtin_fmaf((float)acc * sa, sb, bias);
 }
 
+// As in the other families. exp(-x) passes binary32's range below -88.7, where
+// the result counts as 0 (exactly: at most 2^-121).
 __device__ __forceinline__ float i8_silu(float x) { return x / (1.0f + expf(-x)); }
 
 // Four values to bf16 (v_cvt_pk_bf16_f32: nearest even).
@@ -109,9 +113,11 @@ constexpr int kRowWaves = 8;
 // Up to 16 rows and few columns: fragments straight from memory, the K range
 // split over the eight waves of a workgroup that owns 16 columns of Y. Bound by
 // the weights' bytes: 16 KiB of loads in flight per CU at once and no barrier
-// in the loop (1 x 4096 x 4096: 5.5 us, 3.3 us of it loop = 5 TB/s; two
-// column tiles per workgroup 7.5 us, the 64 x 64 LDS tiles 9.9 us; from 8192
-// columns on those are as fast, at 14336 faster: 12.2 against 17 us).
+// in the loop (1 x 4096 x 4096, weights in the last-level cache: 5.5 us, 3.3 us
+// of it loop = 5 TB/s, from memory 7.2 us; cached also two column tiles per
+// workgroup 7.5 us, the 64 x 64 LDS tiles 9.9 us; from 8192 columns on those are
+// as fast, at 14336 faster: 12.2 against 17 us). K stays in one workgroup, so
+// that few columns leave CUs idle (1 x 576 x 7168, 36 workgroups: 7.0 us).
 template <bool SILU, bool ZP>
 __global__ __launch_bounds__(64 * kRowWaves) void gemm_i8_rows_kernel(const I8Args p) {
   constexpr int KW = kRowWaves, NT = SILU ? 2 : 1;  // gate and up tile
@@ -218,10 +224,11 @@ __global__ __launch_bounds__(256) void gemm_i8_reduce_kernel(const I8Args p, int
 // different banks without padding.
 //
 // What bounds them: the 256 x 256 tile the card's power (8192^3: 2.3-2.4 POP/s
-// with random codes, 3.1 with A all zero; 4096 x 14336 x 4096 239-247 us = 2.0
+// with random codes, 3.1 with A all zero; 4096 x 14336 x 4096 240-265 us = 1.8-2.0
 // POP/s); the small tiles the copies into LDS (16-20 TB/s
 // over the card, so a 64 x 64 tile takes 0.19 us a group where its MFMAs take 0.06);
-// with up to 64 rows HBM (16 x 14336 x 4096 11.8 us = 5.0 TB/s). Row strides
+// with up to 64 rows the weights' way in (16 x 14336 x 4096 16.6 us = 3.6 TB/s from
+// memory, 11.8 us = 5.0 TB/s out of the last-level cache). Row strides
 // that are no multiple of 128 bytes split every copied piece over two lines:
 // up to 1.6 times slower in the small tiles. Measured without gain: eight
 // stages instead of four, eight waves sharing the steps of a group, copies of
@@ -265,9 +272,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t i8_rows_rsrc(const int8_t* bas
 // Copies FROM .. TO - 1 of group g into one stage (every wave issues the same
 // number). TAG, here and below, is not used: it gives every calling function
 // its own specialization (hipcc's host pass rejects a second function that
-// calls the same specialization of a device function using target builtins). Buffer loads, because the compiler tracks them apart from LDS
-// reads; a global load to LDS in flight makes it wait for every LDS read
-// where one would do.
+// calls the same specialization of a device function using target builtins).
+// Buffer loads, because the compiler tracks them apart from LDS reads; a
+// global load to LDS in flight makes it wait for every LDS read where one
+// would do.
 template <int FROM, int TO, int LOADS, int NW, int TAG>
 __device__ __forceinline__ void i8_load_stage(char* st, const I8Src<LOADS>& src, int wave, int g) {
 #pragma unroll
@@ -716,13 +724,14 @@ hipError_t launch_tile(const I8Args& a, bool silu, int m_blocks, int split, hipS
 // take R (G group + round) + 3 us. group: measured microseconds for a
 // 128-byte group of K with the tiles filling the card once, and (many) where
 // several rounds of tiles no longer find their operands in L2; round: a
-// round's prologue and epilogue. Measured in microseconds, bf16 output:
-//                    64x64  128x64  128x128  128x256  256x256
-//    256 x  4096 x 4096   10.9    15.6     20.1       37       53
-//    256 x 14336 x 4096     29      26       22       37       60
-//   1024 x  4096 x 4096     30      27       25       39       55
-//   2048 x  4096 x 4096     63      66       44       38       55
-//   4096 x  4096 x 4096                      93       83       66
+// round's prologue and epilogue. Measured in microseconds, bf16 output, no
+// zero points, operands from memory (the model's rates are of cached ones):
+//                        64x64  128x64  128x128  128x256  256x256
+//    256 x  4096 x 4096   13.4    17.3     22.0     32.6     53.6
+//    256 x 14336 x 4096   36.9    35.1     26.9     35.9     55.3
+//   1024 x  4096 x 4096   37.2    32.3     24.2     33.5     54.1
+//   2048 x  4096 x 4096   70.7    63.5     47.1     38.1     55.5
+//   4096 x  4096 x 4096  124.4   122.9     89.8     74.9     63.5
 // A split adds a second kernel and the partials' traffic (64 x 512 x 16384,
 // 64 x 64: 25.4 us whole, 7.6 + 4.2 us in eight).
 enum I8Kernel { I8_ROWS, I8_64X64, I8_128X64, I8_128X128, I8_128X256, I8_256X256 };
@@ -769,8 +778,9 @@ I8Choice choose_dense(int64_t M, int64_t vcols, int64_t k) {
       }
     }
     // Whole rounds of this tile, and what the last round would hold of it in
-    // smaller ones: 4096 x 14336 x 4096 is 3.5 rounds of 256 x 256 tiles
-    // (259 us in four, 247 with the rest in 128 x 256), 4096 x 4608 x 4096 1.1 (120, 86 us)
+    // smaller ones: 4096 x 4608 x 4096 is 1.1 rounds of 256 x 256 tiles (118 us
+    // in two, 91 with the rest in 128 x 64, zero points); 4096 x 14336 x 4096
+    // 3.5 (266, 265 us)
     const int64_t full = tiles / kCus, n_main = m_blocks > 0 ? full * kCus / m_blocks : 0;
     if (tiles % kCus == 0 || n_main < 1 || n_main >= n_blocks) continue;
     for (const I8Tile& r : kI8Tiles) {

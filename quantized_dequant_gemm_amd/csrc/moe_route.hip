@@ -21,13 +21,15 @@
 // whole token is routed in binary64. Without a bias the keys are the logits:
 // exact for 16-bit types, cut by the index bits for binary32 ones.
 //
-// Error bounds (with a factor of two or more to spare): exp as v_exp_f32 of
-// x * log2(e) is off by 2^-23 + 1.5 |x| 2^-24 relative. Sigmoid: 1 / (1 + t)
-// adds 2^-24 + 2^-23 and passes on s (1 - s) of t's error, and s (1 - s) |x|
-// < 0.3: off by less than 2^-21 absolute. Softmax subtracts first (|d| 2^-24
-// more, s |d| < 0.4) and divides by a sum whose terms with mass have |d|
-// below about ln(1024): less than 2^-20. score_err is twice that, and the bias
-// added rounds by 2^-24 of the key.
+// Error bounds: exp as v_exp_f32 of x * log2(e) is off by 2^-23 + 1.5 |x| 2^-24
+// relative. Sigmoid: 1 / (1 + t) adds 2^-24 + 2^-23 and passes on s (1 - s) of
+// t's error, and s (1 - s) |x| < 0.3: off by less than 2^-21 absolute, half of
+// score_err. Softmax, in units of 2^-24 and with d = x - top: the numerator
+// (2 + 2.5 |d|) s, where s |d| < 0.4; the sum of 1024 terms 21 s for 15
+// additions a lane and 6 across, and (2 + 2.5 D) s for its terms, D the mean of
+// |d| under s; reciprocal and product 3 s. For 1024 experts 28 s + 1 + 2.5 D s
+// stays below 30, score_err is 32. The bias added rounds by 2^-24 of the key,
+// which key_low and key_high count.
 //
 // The weights of the top_k, one lane each: exp in binary32 (one unit in the
 // last place, 2^-23) of the argument's upper part, times 1 + its lower part;
@@ -536,7 +538,9 @@ hipError_t launch_moe_route(const qdg_route_config& c, const void* logits, int64
     return hipGetLastError();
   };
   // one instance for each score, with and without bias and groups: a single
-  // one for all spilled scalar registers (8192 x 256 grouped 18.0 us)
+  // one for all spilled scalar registers at 256 experts (8192 x 256 grouped
+  // 18.0 us). Of these only softmax with a bias at more than 512 experts does,
+  // 20 of them, 32 with groups, into vector registers.
   auto pick = [&](auto experts_per_lane) {
     constexpr int N = decltype(experts_per_lane)::value;
     const bool sg = c.score == QDG_SCORE_SIGMOID, gr = c.num_groups > 1;
