@@ -536,7 +536,8 @@ qdg_status qdg_moe_combine_bf16(const void* y, const float* w, int64_t T, int32_
    Keys and group values decide as in binary64 (a choice between two that
    binary32 cannot tell apart is not left to its rounding); the weights are
    within 2^-21 of their exact values (relative; a subnormal one within half
-   a step of binary32).
+   a step of binary32). Scores below 2^-1022 count with the bits that a
+   subnormal binary64 number has left, also in renormalised weights.
    Masked experts: a logit of -infinity or NaN, or a bias of -infinity or
    NaN, masks an expert: its score is 0, it ranks behind every expert that
    is not masked and adds nothing to a group's value (a group of masked
