@@ -659,6 +659,130 @@ qdg_status qdg_moe_gemm_i8(const qdg_i8_config* cfg, const int8_t* A, const floa
                            const int32_t* block_expert, const int32_t* num_padded, int64_t T, int32_t top_k,
                            int32_t block_m, int32_t a_per_pair, void* Y, void* stream);
 
+/* ------------------------------------------------- rows around the products
+   What stands between two quantized products of a served layer, besides the
+   products themselves (the pages fix none of it; the rules are this
+   library's): norms with gate and residual, gated activations, and low-rank
+   adapters. The first two end in bf16 rows, in the codes that the next product
+   reads, or in both:
+     rows    out bf16 [M][n], row stride ldo elements
+     codes   of the bf16 values, by the rules of the activation quantizers
+             and bit for bit what those give for the same rows:
+       INT8      i8 [M][n], a_scales f32 [M]           (qdg_quantize_act)
+       INT8_ZP   i8 [M][n], a_scales f32 [M], a_zeros i32 [M]
+                                                       (qdg_quantize_act_zp)
+       FP8E4M3   u8 [M][n], a_scales f32 [M][n/128]    (n a multiple of 128)
+       MXFP4     u8 [M][n/2], a_scales u8 [M][n/32]    (n a multiple of 32)
+             qa 16-byte aligned, row stride ldq bytes (a multiple of 16;
+             bytes behind a row's codes stay as they were); scales contiguous
+   Values are decided in binary64 and rounded once to binary32 and from there
+   to bf16 (products of binary32 numbers are exact there, sums and functions
+   correct to 2^-46 of their largest term), so rows, codes and the residual are
+   reproducible bit for bit but for values that close to a border. Infinities
+   and NaN go the way of IEEE arithmetic.
+   Rows may start at any element: pointers other than qa are aligned to their
+   elements only. An output may not overlap an input or another output, but
+   for residual_out = residual (the stream updated in place, lds = ldr) and
+   out = x (both bf16, ldo = ldx). Device pointers; one launch, no workspace;
+   M = 0 enqueues nothing. */
+enum { QDG_Q_NONE = 0, QDG_Q_INT8 = 1, QDG_Q_INT8_ZP = 2, QDG_Q_FP8E4M3 = 3, QDG_Q_MXFP4 = 4 };
+
+/* Norms around a block, with its gate and the residual stream:
+     t = x                       or, with post_norm, N(x; post_weight, post_bias)
+     s = residual_scale * residual + gate * t, rounded to rtype: residual_out
+     y = N(s; weight, bias): rows and codes (both absent: s alone is wanted)
+   N over the n values of a row, mean and variance without correction:
+     RMS    v / sqrt(mean(v^2) + eps) * (w + weight_offset) + b
+     LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * (w + weight_offset) + b
+   A weight that is NULL is left out with its offset (factor 1); a NULL bias,
+   gate or residual likewise (0, 1, 0). weight_offset 1 is for weights that are
+   stored as their distance from 1.
+   x [M][n] of xtype, residual and residual_out [M][n] of rtype (BF16 or F32),
+   gate [M][n] with row stride ldg, or one row for all with ldg = 0; gate,
+   weights and biases [n] of wtype (BF16 or F32). n in [1, 32768]; eps >= 0,
+   eps, residual_scale and weight_offset finite. A row of zeros with eps = 0 is
+   0 / 0: NaN. */
+enum { QDG_NORM_RMS = 0, QDG_NORM_LAYER = 1 };
+typedef struct qdg_norm_config {
+  int64_t n;
+  int64_t ldx, ldr, lds, ldg, ldo, ldq; /* x, residual, residual_out, gate, out (elements), qa (bytes) */
+  int32_t kind, post_norm;              /* QDG_NORM_*; 0 or 1 */
+  int32_t xtype, rtype, wtype;          /* QDG_O_BF16 or QDG_O_F32 */
+  int32_t quant;                        /* QDG_Q_* */
+  float eps, residual_scale, weight_offset;
+  int32_t reserved;                     /* 0 */
+} qdg_norm_config;
+
+/* residual, gate, post_weight, post_bias, weight, bias, residual_out and out
+   may be NULL (post_weight and post_bias have to be without post_norm); qa and
+   a_scales are needed with codes, a_zeros with INT8_ZP; strides of absent
+   tensors are not looked at. At least one of residual_out, out and codes.
+   Errors: QDG_ERR_INVALID_ARG, QDG_ERR_MISALIGNED, QDG_ERR_UNSUPPORTED
+   (n > 32768, M >= 2^31, n no whole groups of the codes). */
+qdg_status qdg_norm(const qdg_norm_config* cfg, const void* x, const void* residual, const void* gate,
+                    const void* post_weight, const void* post_bias, const void* weight, const void* bias, int64_t M,
+                    void* residual_out, void* out, void* qa, void* a_scales, int32_t* a_zeros, void* stream);
+
+/* Gated activation of a gate+up projection whose product left plain rows (an
+   adapter has to be added before the activation, or the codes are wanted):
+     y = act(g) * u,  g = Y[m][0 .. n), u = Y[m][n .. 2n)
+     SILU       g / (1 + exp(-g))
+     GELU_TANH  0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
+   Y [M][2n] of ytype (BF16 or F32), row stride ldy elements. n in [1, 65536].
+   out and codes as above, at least one of them. Errors as for qdg_norm. */
+enum { QDG_ACT_SILU = 0, QDG_ACT_GELU_TANH = 1 };
+typedef struct qdg_gated_config {
+  int64_t n;
+  int64_t ldy, ldo, ldq;
+  int32_t act, ytype, quant, reserved; /* reserved: 0 */
+} qdg_gated_config;
+qdg_status qdg_gated_act(const qdg_gated_config* cfg, const void* Y, int64_t M, void* out, void* qa, void* a_scales,
+                         int32_t* a_zeros, void* stream);
+
+/* Low-rank adapters of many requests beside a projection that all rows share:
+   to the rows of Y that a product has left,
+     Y[m][j] += scales[a] * sum_r (sum_k X[m][k] * A[a][slice(j)][r][k]) * B[a][j][r]
+   for a the adapter of row m and r < ranks[a]. Rows are grouped as experts'
+   are: sorted_ids, block_adapter and num_padded are those of
+   qdg_moe_align(ids, M, 1, num_adapters, block_m) over each row's adapter; a
+   row whose id is outside [0, num_adapters), -1 for no adapter, is left out
+   and stays as it was. One grouping serves every projection of a step.
+   A stacked projection (q, k and v; gate and up) has a slice for each part:
+   columns [slice_end[i-1], slice_end[i]) of Y belong to slice i and have an A
+   of their own.
+   X bf16 [M][k], row stride ldx; A bf16 [num_adapters][num_slices][rank][k], B
+   bf16 [num_adapters][n][rank], contiguous; ranks i32 [num_adapters] (clamped
+   to 0 .. rank; entries of A and B behind an adapter's rank may hold anything)
+   or NULL (all rank); scales f32 [num_adapters] or NULL (all 1); Y [M][n] of
+   otype BF16 or F32, row stride ldy. All aligned to their elements.
+   Products of bf16 numbers are exact in binary32 and are added there; the
+   inner sums enter the second product, scaled, with 16 bits of their
+   significand (2^-18 of their value); the sum joins Y in binary32 and is
+   rounded once to otype. Results do not depend on other rows' values, but their
+   last bits may on M and the grouping (the order of the inner sums).
+   n, k in [1, 2^26]; rank 1..256; num_slices 1..4, slice_end ascending, the
+   last one n; num_adapters 1..1024; M in [0, 2^20] (0 enqueues nothing);
+   block_m 16, 32, 64 or 128: the smaller while adapters hold few rows each
+   (about 32 rows an adapter: 16 up to there, 64 beyond). */
+typedef struct qdg_lora_config {
+  int64_t n, k, ldx, ldy;
+  int64_t slice_end[4];
+  int32_t num_adapters, num_slices, rank, otype;
+} qdg_lora_config;
+
+/* Workspace bytes that serve qdg_lora for M rows and for any fewer (the inner
+   sums in binary32). The contents need no initialisation. Calls that share a
+   workspace must be ordered on one stream. */
+qdg_status qdg_lora_workspace(const qdg_lora_config* cfg, int64_t M, int32_t block_m, size_t* bytes);
+
+/* workspace 16-byte aligned. Errors: QDG_ERR_INVALID_ARG, QDG_ERR_MISALIGNED,
+   QDG_ERR_WORKSPACE, QDG_ERR_UNSUPPORTED (another block_m, a size past the
+   ranges above, more tiles than one launch holds). */
+qdg_status qdg_lora(const qdg_lora_config* cfg, const void* X, const void* A, const void* B, const int32_t* ranks,
+                    const float* scales, const int32_t* sorted_ids, const int32_t* block_adapter,
+                    const int32_t* num_padded, int64_t M, int32_t block_m, void* Y, void* workspace, size_t ws_bytes,
+                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

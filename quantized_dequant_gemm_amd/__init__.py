@@ -29,6 +29,9 @@ QDG_FLAG_BAD_SCALE, QDG_FLAG_BAD_ZERO_POINT, QDG_FLAG_BAD_EXPERT_ID, QDG_FLAG_BA
 QDG_L_BF16, QDG_L_F16, QDG_L_F32 = range(3)
 QDG_SCORE_SOFTMAX, QDG_SCORE_SIGMOID = range(2)
 QDG_GROUP_MAX, QDG_GROUP_TOP2 = range(2)
+QDG_Q_NONE, QDG_Q_INT8, QDG_Q_INT8_ZP, QDG_Q_FP8E4M3, QDG_Q_MXFP4 = range(5)
+QDG_NORM_RMS, QDG_NORM_LAYER = range(2)
+QDG_ACT_SILU, QDG_ACT_GELU_TANH = range(2)
 
 STATUS_NAMES = {0: "QDG_OK", 1: "QDG_ERR_INVALID_ARG", 2: "QDG_ERR_UNSUPPORTED", 3: "QDG_ERR_MISALIGNED",
                 4: "QDG_ERR_WORKSPACE", 5: "QDG_ERR_HIP"}
@@ -40,7 +43,8 @@ EXPORTS = (
     "qdg_plan_describe", "qdg_moe_describe", "qdg_gemm", "qdg_moe_align_capacity", "qdg_moe_align",
     "qdg_moe_gemm", "qdg_moe_combine", "qdg_moe_combine_bf16", "qdg_plan_autotune", "qdg_plan_autotune_reset",
     "qdg_plan_jit", "qdg_gemm_noalloc", "qdg_moe_route", "qdg_quantize_act_zp", "qdg_gemm_i8_workspace",
-    "qdg_gemm_i8_describe", "qdg_gemm_i8", "qdg_moe_gemm_i8",
+    "qdg_gemm_i8_describe", "qdg_gemm_i8", "qdg_moe_gemm_i8", "qdg_norm", "qdg_gated_act",
+    "qdg_lora_workspace", "qdg_lora",
 )
 
 
@@ -77,6 +81,26 @@ class I8Config(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
                 ("ldy", ctypes.c_int64), ("num_experts", ctypes.c_int32), ("otype", ctypes.c_int32),
                 ("epilogue", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("lds", ctypes.c_int64),
+                ("ldg", ctypes.c_int64), ("ldo", ctypes.c_int64), ("ldq", ctypes.c_int64), ("kind", ctypes.c_int32),
+                ("post_norm", ctypes.c_int32), ("xtype", ctypes.c_int32), ("rtype", ctypes.c_int32),
+                ("wtype", ctypes.c_int32), ("quant", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class GatedConfig(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldo", ctypes.c_int64), ("ldq", ctypes.c_int64),
+                ("act", ctypes.c_int32), ("ytype", ctypes.c_int32), ("quant", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class LoraConfig(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("slice_end", ctypes.c_int64 * 4), ("num_adapters", ctypes.c_int32), ("num_slices", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("otype", ctypes.c_int32)]
 
 
 class QdgError(RuntimeError):
@@ -126,6 +150,10 @@ def load():
         "qdg_gemm_i8_describe": (ctypes.c_int, [P, I64, ctypes.c_char_p, SZ]),
         "qdg_gemm_i8": (I32, [P, P, P, P, P, P, P, P, I64, P, SZ, P]),
         "qdg_moe_gemm_i8": (I32, [P, P, P, P, P, P, P, P, P, P, I64, I32, I32, I32, P, P]),
+        "qdg_norm": (I32, [P] * 8 + [I64] + [P] * 6),
+        "qdg_gated_act": (I32, [P, P, I64, P, P, P, P, P]),
+        "qdg_lora_workspace": (I32, [P, I64, I32, P]),
+        "qdg_lora": (I32, [P] * 9 + [I64, I32, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -336,6 +364,28 @@ def qdg_moe_gemm_i8(cfg, A, a_scales, a_zeros, B, b_scales, bias, sorted_ids, bl
                                   block_expert, num_padded, T, top_k, block_m, a_per_pair, Y, stream))
 
 
+def qdg_norm(cfg, x, residual, gate, post_weight, post_bias, weight, bias, M, residual_out, out, qa=None,
+             a_scales=None, a_zeros=None, stream=0):
+    _check(load().qdg_norm(ctypes.byref(cfg), x, residual, gate, post_weight, post_bias, weight, bias, M, residual_out,
+                           out, qa, a_scales, a_zeros, stream))
+
+
+def qdg_gated_act(cfg, Y, M, out, qa=None, a_scales=None, a_zeros=None, stream=0):
+    _check(load().qdg_gated_act(ctypes.byref(cfg), Y, M, out, qa, a_scales, a_zeros, stream))
+
+
+def qdg_lora_workspace(cfg, M, block_m):
+    out = ctypes.c_size_t()
+    _check(load().qdg_lora_workspace(ctypes.byref(cfg), M, block_m, ctypes.byref(out)))
+    return out.value
+
+
+def qdg_lora(cfg, X, A, B, ranks, scales, sorted_ids, block_adapter, num_padded, M, block_m, Y, workspace, ws_bytes,
+             stream=0):
+    _check(load().qdg_lora(ctypes.byref(cfg), X, A, B, ranks, scales, sorted_ids, block_adapter, num_padded, M,
+                           block_m, Y, workspace, ws_bytes, stream))
+
+
 # ------------------------------------------------------------- config helpers
 
 def route(num_experts, top_k, ltype=QDG_L_BF16, score=QDG_SCORE_SOFTMAX, num_groups=1, topk_groups=1,
@@ -350,6 +400,34 @@ def gemm_i8(n, k, lda=None, ldb=None, ldy=None, num_experts=1, otype=QDG_O_BF16,
     return I8Config(n=n, k=k, lda=lda or k16, ldb=ldb or k16,
                     ldy=ldy or (n // 2 if epilogue == QDG_EPI_SILU_MUL else n), num_experts=num_experts,
                     otype=otype, epilogue=epilogue, reserved=0)
+
+
+def norm(n, kind=QDG_NORM_RMS, xtype=QDG_O_BF16, rtype=QDG_O_BF16, wtype=QDG_O_BF16, post_norm=0, quant=QDG_Q_NONE,
+         eps=1e-5, residual_scale=1.0, weight_offset=0.0, ldx=None, ldr=None, lds=None, ldg=0, ldo=None, ldq=None):
+    """Strides default to contiguous rows, ldq to a row's codes rounded up to 16 bytes; ldg 0: one gate row for all."""
+    return NormConfig(n=n, ldx=n if ldx is None else ldx, ldr=n if ldr is None else ldr, lds=n if lds is None else lds,
+                      ldg=ldg, ldo=n if ldo is None else ldo, ldq=_code_stride(n, quant) if ldq is None else ldq,
+                      kind=kind, post_norm=post_norm, xtype=xtype, rtype=rtype, wtype=wtype, quant=quant, eps=eps,
+                      residual_scale=residual_scale, weight_offset=weight_offset, reserved=0)
+
+
+def gated_act(n, act=QDG_ACT_SILU, ytype=QDG_O_BF16, quant=QDG_Q_NONE, ldy=None, ldo=None, ldq=None):
+    """Strides default to contiguous rows, ldq to a row's codes rounded up to 16 bytes."""
+    return GatedConfig(n=n, ldy=2 * n if ldy is None else ldy, ldo=n if ldo is None else ldo,
+                       ldq=_code_stride(n, quant) if ldq is None else ldq, act=act, ytype=ytype, quant=quant,
+                       reserved=0)
+
+
+def _code_stride(n, quant):
+    return ((n // 2 if quant == QDG_Q_MXFP4 else n) + 15) // 16 * 16
+
+
+def lora(n, k, rank, num_adapters=1, slice_ends=None, otype=QDG_O_BF16, ldx=None, ldy=None):
+    """slice_ends: the ends of a stacked projection's parts (default: one part, [n])."""
+    ends = [n] if slice_ends is None else list(slice_ends)
+    return LoraConfig(n=n, k=k, ldx=k if ldx is None else ldx, ldy=n if ldy is None else ldy,
+                      slice_end=(ctypes.c_int64 * 4)(*ends[:4]), num_adapters=num_adapters, num_slices=len(ends),
+                      rank=rank, otype=otype)
 
 
 def layer_w4a16(n, k, asym=False, num_experts=1, otype=QDG_O_BF16):

@@ -15,20 +15,14 @@
 // (v_cvt_pk_fp8_f32, v_cvt_scalef32_pk_fp4_f32: round to nearest even, the
 // sign kept on zero); the tests compare them with the oracle's encoders over
 // every bf16 input magnitude the encodes can see.
-#include "qdg_device.h"
+#include "qdg_codes.h"
 #include "qdg_internal.h"
 
 namespace qdg {
 namespace {
 
-__device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __builtin_bit_cast(float, h << 16); }
-
-
 // MXFP4 per (token, 32-block): four lanes per block, 8 values (16 bytes) each;
-// the block's amax comes from a 4-lane reduction. X is read from the
-// exponent field of amax (a subnormal amax, below 2^-126, gives the clamped
-// X = -127), and x / 2^X is a product with the power of two 2^-X, exact for
-// every value whose code is not 0.
+// the block's amax comes from a 4-lane reduction.
 __global__ __launch_bounds__(256) void act_fp4_kernel(const uint16_t* __restrict__ a, uint8_t* __restrict__ q,
                                                       uint8_t* __restrict__ scales, int64_t blocks) {
   const int64_t gl = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -49,19 +43,8 @@ __global__ __launch_bounds__(256) void act_fp4_kernel(const uint16_t* __restrict
   amax = fmaxf(amax, __shfl_xor(amax, 2, 4));
   uint32_t out = 0, e8 = 0;
   if (amax > 0.f) {
-    const int ef = (int)((__builtin_bit_cast(uint32_t, amax) >> 23) & 0xFFu);
-    int X = ef == 0 ? -127 : ef - 127 - 2;  // floor(log2(amax)) - 2
-    X = X < -127 ? -127 : X;
-    e8 = (uint32_t)(X + 127);
-    const float inv = __builtin_bit_cast(float, (uint32_t)(127 - X) << 23);  // 2^-X, X in [-127, 125]
-    // gfx950's v_cvt_scalef32_pk_fp4_f32 encodes two binary32 values as
-    // E2M1 with round to nearest even and saturation at +-6 (sign kept for
-    // values that round to zero); with scale 1 it encodes x / 2^X itself,
-    // element 2j in the low nibble of byte j
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, f[0] * inv, f[1] * inv, 1.0f, 0);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, f[2] * inv, f[3] * inv, 1.0f, 1);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, f[4] * inv, f[5] * inv, 1.0f, 2);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, f[6] * inv, f[7] * inv, 1.0f, 3);
+    e8 = fp4_block_exponent(amax);
+    out = encode_fp4x8(f, e8);
   }
   *(uint32_t*)(q + b * 16 + sub * 4) = out;
   if (sub == 0) scales[b] = (uint8_t)e8;
@@ -92,16 +75,13 @@ __global__ __launch_bounds__(256) void act_int8_kernel(const uint16_t* __restric
   int8_t* y = q + row * K;
   for (int64_t k = threadIdx.x * 8; k < K; k += 256 * 8) {
     const u32x4_t v = *(const u32x4_t*)(x + k);
-    u32x2_t out;
+    float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float f0 = fminf(fmaxf(rintf(bf16_to_f32(v[i] & 0xFFFFu) * inv), -127.f), 127.f);
-      const float f1 = fminf(fmaxf(rintf(bf16_to_f32(v[i] >> 16) * inv), -127.f), 127.f);
-      const uint32_t b = ((uint32_t)(int)f0 & 0xFFu) | (((uint32_t)(int)f1 & 0xFFu) << 8);
-      if (i & 1) out[i >> 1] |= b << 16;
-      else out[i >> 1] = b;
+      f[2 * i] = bf16_to_f32(v[i] & 0xFFFFu);
+      f[2 * i + 1] = bf16_to_f32(v[i] >> 16);
     }
-    *(u32x2_t*)(y + k) = out;
+    *(u32x2_t*)(y + k) = encode_int8x8(f, inv);
   }
 }
 
@@ -128,22 +108,7 @@ __global__ __launch_bounds__(256) void act_fp8_kernel(const uint16_t* __restrict
   const bool nz = amax > 0.f;
   const float inv = nz ? __fdiv_rn(448.0f, amax) : 0.f;
   if (sub == 0) scales[row * groups + g] = nz ? __fdiv_rn(amax, 448.0f) : 1.0f;
-  // gfx950's v_cvt_pk_fp8_f32 encodes two binary32 values as OCP E4M3 with
-  // round to nearest even (subnormal codes included, the sign kept for
-  // values that round to zero); inputs are clamped to the largest finite
-  // magnitude first, so no code is NaN
-  u32x2_t out = {0, 0};
-  if (nz) {
-    float t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = fminf(fmaxf(f[i] * inv, -448.f), 448.f);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * j], t[4 * j + 1], 0, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * j + 2], t[4 * j + 3], w, true);
-      out[j] = (uint32_t)w;
-    }
-  }
+  const u32x2_t out = nz ? encode_fp8x8(f, inv) : u32x2_t{0, 0};
   *(u32x2_t*)(q + row * K + g * 128 + sub * 8) = out;
 }
 
@@ -204,26 +169,6 @@ namespace {
 // chunks of 16 values each) between the range and the encoding, so it is read once.
 // M = 4096, k = 14336: 40.6 us (4.3 TB/s); 53.7 us with a second read and binary64
 // throughout.
-//
-// Range: a bf16 word as int16 orders the values from 0 up, as uint16 the
-// negative ones by magnitude above all others, so hi and lo are packed
-// 16-bit maxima; an infinity or a NaN shows as a maximum past the largest
-// finite word, and only then the row's values are checked one by one.
-// Encoding: y = fma(x, inv32, 1.5 * 2^23) carries rne(x * inv32) in its low
-// bits. inv32 is off by 2^-24 of itself and |x * inv| <= 256, so the code is the
-// binary64 one unless x * inv32 is within 2^-16 of the middle between two
-// integers (kDoubt = 2^-15 is used); a chunk with such a value (or NaN) is encoded again
-// in binary64: one chunk of 64 lanes in 16.
-constexpr float kDoubt = 0.5f - 0x1p-15f;
-
-__device__ __forceinline__ uint32_t pk_max_i16(uint32_t a, uint32_t b) {
-  typedef __attribute__((ext_vector_type(2))) short i16x2_t;
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(i16x2_t, a), __builtin_bit_cast(i16x2_t, b)));
-}
-__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
-  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2_t;
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
-}
 
 // 16 values of a row from i on (dword d holds values 2 d and 2 d + 1), 0
 // behind its end. The 16 bytes at i and at i + 8 are read only where they
@@ -242,47 +187,10 @@ __device__ __forceinline__ void load16(const uint16_t* x, int64_t i, int64_t k, 
   }
 }
 
-struct ZpRow {
-  float scale, inv32;
-  double inv, zero;
-};
-
-__device__ __forceinline__ ZpRow zp_row(float lo, float hi) {
-  const bool any = hi > lo;
-  ZpRow z;
-  z.scale = any ? fmaxf((float)(((double)hi - (double)lo) / 255.0), 0x1p-126f) : 1.0f;
-  z.inv = 1.0 / (double)z.scale;
-  z.inv32 = (float)z.inv;
-  z.zero = any ? fmin(fmax(rint(-128.0 - (double)lo * z.inv), -128.0), 127.0) : 0.0;
-  return z;
-}
-
 // The codes of 16 values into q + i.
 __device__ __forceinline__ void encode16(const uint32_t (&v)[8], const ZpRow& z, int8_t* q, int64_t i, int64_t k) {
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-  const int shift = (int)z.zero - 0x4B400000;
   uint32_t out[4];
-  bool doubt = false;
-  int c[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float f = __builtin_bit_cast(float, j & 1 ? v[j >> 1] & 0xFFFF0000u : v[j >> 1] << 16);
-    const float y = __builtin_fmaf(f, z.inv32, kMagic);
-    doubt |= !(fabsf(__builtin_fmaf(f, z.inv32, kMagic - y)) < kDoubt);
-    c[j] = min(max(__builtin_bit_cast(int, y) + shift, -128), 127);
-  }
-  if (doubt) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float f = __builtin_bit_cast(float, j & 1 ? v[j >> 1] & 0xFFFF0000u : v[j >> 1] << 16);
-      const double d = f == f ? rint((double)f * z.inv) : 0.0;
-      c[j] = (int)fmin(fmax(d + z.zero, -128.0), 127.0);
-    }
-  }
-#pragma unroll
-  for (int d = 0; d < 4; ++d)
-    out[d] = ((uint32_t)c[4 * d] & 0xFFu) | ((uint32_t)c[4 * d + 1] & 0xFFu) << 8 |
-             ((uint32_t)c[4 * d + 2] & 0xFFu) << 16 | (uint32_t)c[4 * d + 3] << 24;
+  encode_zp<8>(v, z, out);
   if (i + 16 <= k) {
     *(u32x4_t*)(q + i) = u32x4_t{out[0], out[1], out[2], out[3]};
   } else {
@@ -349,23 +257,13 @@ __global__ __launch_bounds__(256) void act_int8_zp_kernel(const uint16_t* __rest
     row_max2<TPR>(hw, lw, buf);
     if (hw >= 0x7F80u || lw >= 0xFF80u) {  // an infinity or a NaN: they do not count
       hw = lw = 0;
-      auto finite_max = [&](const uint32_t(&w)[8]) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t h = j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu;
-          if ((h & 0x7FFFu) < 0x7F80u) {
-            if (h < 0x8000u) hw = max(hw, h);
-            lw = max(lw, h);
-          }
-        }
-      };
       if constexpr (CH > 0) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) finite_max(v[c]);
+        for (int c = 0; c < CH; ++c) zp_finite_max<8>(v[c], hw, lw);
       } else {
         for (int c = 0; c < chunks; ++c) {
           load16(x, ((int64_t)c * TPR + t) * 16, k, v[0]);
-          finite_max(v[0]);
+          zp_finite_max<8>(v[0], hw, lw);
         }
       }
       row_max2<TPR>(hw, lw, buf);

@@ -202,6 +202,69 @@ I8Instance gemm_i8_instance(int64_t M, int64_t vcols, int64_t k);
 hipError_t launch_gemm_i8(const I8Args& a, bool silu, hipStream_t s);
 hipError_t launch_moe_gemm_i8(const I8Args& a, bool silu, int m_blocks, hipStream_t s);
 
+// Where a row operator leaves its rows: bf16 values (rows NULL: none) and
+// codes of one of the activation quantizers (quant QDG_Q_*).
+struct RowOut {
+  uint16_t* rows;
+  int64_t ld;
+  uint8_t* qa;
+  int64_t ldq;      // bytes
+  void* scales;
+  int32_t* zeros;
+  int quant;
+};
+struct NormArgs {
+  const void* x;
+  const void* residual;     // NULL: none
+  const void* gate;         // NULL: 1; ldg 0: one row for all
+  const void* post_weight;
+  const void* post_bias;
+  const void* weight;
+  const void* bias;
+  void* residual_out;       // NULL: not kept
+  int64_t ldx, ldr, ldg, lds, M;
+  int n;
+  bool layer, post_norm, wf32;
+  float eps, residual_scale, weight_offset;
+  RowOut out;
+};
+struct GatedArgs {
+  const void* y;
+  int64_t ldy, M;
+  int n, act;
+  RowOut out;
+};
+hipError_t launch_norm(const NormArgs& a, bool xf32, bool rf32, hipStream_t s);
+hipError_t launch_gated_act(const GatedArgs& a, bool yf32, hipStream_t s);
+
+// Low-rank adapters over rows grouped by adapter.
+struct LoraArgs {
+  const uint16_t* X;
+  const uint16_t* A;       // [adapters][slices][rank][k]
+  const uint16_t* B;       // [adapters][n][rank]
+  const int32_t* ranks;    // NULL: rank
+  const float* scales;     // NULL: 1
+  const int32_t* sorted_ids;
+  const int32_t* block_adapter;
+  const int32_t* num_padded;
+  void* Y;
+  float* partial;          // [split][rows in order][slices * rank_pad]
+  int64_t ldx, ldy;
+  int64_t M;
+  int n, k;
+  int num_adapters, num_slices, rank, rank_pad;
+  int slice_end[4];
+  int block_m, blocks;     // blocks: the most that M rows make
+  int split;
+  bool yf32;
+};
+// The most blocks of block_m rows that M rows of at most E adapters make.
+int64_t lora_blocks(int64_t M, int64_t E, int block_m);
+int lora_rank_pad(int rank);
+int lora_split(int64_t tiles, int columns, int64_t k);
+int64_t lora_expand_units(const LoraArgs& a);
+hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
+
 #endif
 
 }  // namespace qdg
