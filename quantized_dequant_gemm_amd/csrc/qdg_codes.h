@@ -142,6 +142,7 @@ __device__ __forceinline__ void encode_zp(const uint32_t (&v)[ND], const ZpRow& 
       const float f = bf16_pair(v[j >> 1], j);
       const double d = f == f ? rint((double)f * z.inv) : 0.0;
       c[j] = (int)fmin(fmax(d + z.zero, -128.0), 127.0);
+      __builtin_amdgcn_sched_barrier(0);  // one chain at a time: registers
     }
   }
 #pragma unroll

@@ -3,12 +3,15 @@
 // the stream is normed for the next block) and qdg_gated_act (act(gate) * up).
 //
 // Every value is decided in binary64 and rounded once to binary32, from there
-// to bf16, so rows and codes are reproducible bit for bit. Both operators are
-// bound by their bytes: TPR threads hold a row in registers, CH chunks of eight
-// neighbouring values each, so that it is read once whatever statistics the
-// norms and the codes need. Rows may start at any element: the 16-byte loads
-// and stores are unaligned ones, and only a chunk that the row's end cuts is
-// moved by elements.
+// to bf16, so rows and codes are reproducible bit for bit. Sums are binary64;
+// the values themselves are computed in binary32 beside a bound of their error,
+// and only where that leaves the bf16 number open (one value in 3000 to 5000)
+// they are computed again in binary64. Both operators are bound by their bytes:
+// TPR threads hold a row in registers, CH chunks of eight neighbouring values
+// each, so that it is read once whatever statistics the norms and the codes
+// need. Rows may start at any element: the 16-byte loads and stores are
+// unaligned ones; a chunk that the row's end cuts is read as the row's last
+// eight values and shifted.
 #include "qdg_codes.h"
 #include "qdg_internal.h"
 
@@ -17,6 +20,9 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_2_t;
 typedef __attribute__((ext_vector_type(4), aligned(4))) uint32_t u32x4_4_t;
+typedef __attribute__((ext_vector_type(2), aligned(2))) uint32_t u32x2_2_t;
+typedef __attribute__((ext_vector_type(2), aligned(4))) uint32_t u32x2_4_t;
+typedef __attribute__((aligned(2))) uint32_t u32_2_t;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 
 // Eight values of one type as they are stored: bf16 pairs or binary32.
@@ -27,56 +33,124 @@ struct Raw8 {
     if constexpr (F32) return __builtin_bit_cast(float, d[j]);
     else return bf16_pair(d[j >> 1], j);
   }
+  // Keeps the compiler from holding what it has converted from the values
+  // (eight binary64 numbers are 16 registers) until they are needed again.
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int j = 0; j < (F32 ? 8 : 4); ++j) asm volatile("" : "+v"(d[j]));
+  }
 };
 
-// Values i .. i + 7 of a row of n, 0 behind its end.
+// Values i .. i + 7 of a row of n (i < n), 0 behind its end.
 template <bool F32>
 __device__ __forceinline__ Raw8<F32> load8(const void* row, int i, int n) {
   Raw8<F32> r;
-  if (i + 8 <= n) {
-    if constexpr (F32) {
-      const u32x4_4_t a = *(const u32x4_4_t*)((const uint32_t*)row + i), b = *(const u32x4_4_t*)((const uint32_t*)row + i + 4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r.d[j] = a[j];
-        r.d[4 + j] = b[j];
-      }
-    } else {
-      const u32x4_2_t a = *(const u32x4_2_t*)((const uint16_t*)row + i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r.d[j] = a[j];
-    }
-  } else {
+  if (n < 8) {  // the same for all lanes: a row that is no chunk
 #pragma unroll
     for (int j = 0; j < (F32 ? 8 : 4); ++j) {
       if constexpr (F32) {
-        r.d[j] = i + j < n ? ((const uint32_t*)row)[i + j] : 0u;
+        r.d[j] = j < n ? ((const uint32_t*)row)[j] : 0u;
       } else {
-        r.d[j] = i + 2 * j < n ? ((const uint16_t*)row)[i + 2 * j] : 0u;
-        if (i + 2 * j + 1 < n) r.d[j] |= (uint32_t)((const uint16_t*)row)[i + 2 * j + 1] << 16;
+        r.d[j] = 2 * j < n ? ((const uint16_t*)row)[2 * j] : 0u;
+        if (2 * j + 1 < n) r.d[j] |= (uint32_t)((const uint16_t*)row)[2 * j + 1] << 16;
       }
+    }
+    return r;
+  }
+  const int at = min(i, n - 8), skip = i - at;  // values that a chunk before has
+  if constexpr (F32) {
+    const u32x4_4_t a = *(const u32x4_4_t*)((const uint32_t*)row + at), b = *(const u32x4_4_t*)((const uint32_t*)row + at + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r.d[j] = a[j];
+      r.d[4 + j] = b[j];
+    }
+  } else {
+    const u32x4_2_t a = *(const u32x4_2_t*)((const uint16_t*)row + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.d[j] = a[j];
+  }
+  if (skip) {
+    constexpr int kPer = F32 ? 1 : 2, kD = F32 ? 8 : 4;  // values a dword, dwords
+#pragma unroll
+    for (int b = 4; b >= kPer; b >>= 1)
+      if (skip & b)
+#pragma unroll
+        for (int j = 0; j < kD; ++j) r.d[j] = j + b / kPer < kD ? r.d[j + b / kPer] : 0u;
+    if constexpr (!F32) {
+      if (skip & 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.d[j] = r.d[j] >> 16 | (j < 3 ? r.d[j + 1] << 16 : 0u);
     }
   }
   return r;
 }
 
+// The first values of r into values i .. of a row of n (i < n).
 template <bool F32>
-__device__ __forceinline__ void store8(void* row, int i, int n, const Raw8<F32>& r) {
-  if (i + 8 <= n) {
-    if constexpr (F32) {
-      *(u32x4_4_t*)((uint32_t*)row + i) = u32x4_4_t{r.d[0], r.d[1], r.d[2], r.d[3]};
-      *(u32x4_4_t*)((uint32_t*)row + i + 4) = u32x4_4_t{r.d[4], r.d[5], r.d[6], r.d[7]};
-    } else {
-      *(u32x4_2_t*)((uint16_t*)row + i) = u32x4_2_t{r.d[0], r.d[1], r.d[2], r.d[3]};
+__device__ __forceinline__ void store8(void* row, int i, int n, Raw8<F32> r) {
+  if constexpr (F32) {
+    uint32_t* p = (uint32_t*)row + i;
+    if (i + 8 <= n) {
+      *(u32x4_4_t*)p = u32x4_4_t{r.d[0], r.d[1], r.d[2], r.d[3]};
+      *(u32x4_4_t*)(p + 4) = u32x4_4_t{r.d[4], r.d[5], r.d[6], r.d[7]};
+      return;
     }
-  } else {
+    const int rest = n - i;
+    if (rest & 4) {
+      *(u32x4_4_t*)p = u32x4_4_t{r.d[0], r.d[1], r.d[2], r.d[3]};
+      p += 4;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i + j < n) {
-        if constexpr (F32) ((uint32_t*)row)[i + j] = r.d[j];
-        else ((uint16_t*)row)[i + j] = (uint16_t)(r.d[j >> 1] >> (16 * (j & 1)));
-      }
+      for (int j = 0; j < 3; ++j) r.d[j] = r.d[4 + j];
+    }
+    if (rest & 2) {
+      *(u32x2_4_t*)p = u32x2_4_t{r.d[0], r.d[1]};
+      p += 2;
+      r.d[0] = r.d[2];
+    }
+    if (rest & 1) *p = r.d[0];
+  } else {
+    uint16_t* p = (uint16_t*)row + i;
+    if (i + 8 <= n) {
+      *(u32x4_2_t*)p = u32x4_2_t{r.d[0], r.d[1], r.d[2], r.d[3]};
+      return;
+    }
+    const int rest = n - i;
+    if (rest & 4) {
+      *(u32x2_2_t*)p = u32x2_2_t{r.d[0], r.d[1]};
+      p += 4;
+      r.d[0] = r.d[2];
+      r.d[1] = r.d[3];
+    }
+    if (rest & 2) {
+      *(u32_2_t*)p = r.d[0];
+      p += 2;
+      r.d[0] = r.d[1];
+    }
+    if (rest & 1) *p = (uint16_t)r.d[0];
   }
+}
+
+// Eight codes into bytes i .. of a row of n (rows of codes start at a multiple of 16).
+__device__ __forceinline__ void store_codes(uint8_t* row, int i, int n, u32x2_t v) {
+  uint8_t* p = row + i;
+  if (i + 8 <= n) {
+    *(u32x2_t*)p = v;
+    return;
+  }
+  const int rest = n - i;
+  uint32_t w = v.x;
+  if (rest & 4) {
+    *(uint32_t*)p = w;
+    p += 4;
+    w = v.y;
+  }
+  if (rest & 2) {
+    *(uint16_t*)p = (uint16_t)w;
+    p += 2;
+    w >>= 16;
+  }
+  if (rest & 1) *p = (uint8_t)w;
 }
 
 // A pair of binary32 values as bf16, round to nearest even (v_cvt_pk_bf16_f32).
@@ -86,50 +160,129 @@ __device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
 }
 
 // Weights, biases and gates: bf16 or binary32 as the call says.
-__device__ __forceinline__ void load_vec8(const void* p, bool f32, int i, int n, float (&w)[8]) {
-  if (f32) {
+struct Vec8 {
+  float v[8];
+};
+__device__ __forceinline__ Vec8 load_vec8(const void* p, float absent, bool f32, int i, int n) {
+  Vec8 w;
+  if (!p) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w.v[j] = absent;
+  } else if (f32) {
     const Raw8<true> r = load8<true>(p, i, n);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = r[j];
+    for (int j = 0; j < 8; ++j) w.v[j] = r[j];
   } else {
     const Raw8<false> r = load8<false>(p, i, n);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = r[j];
+    for (int j = 0; j < 8; ++j) w.v[j] = r[j];
   }
+  return w;
 }
 
 // ------------------------------------------------------------------ reductions over the TPR threads of a row
+// Lane exchanges of DPP within 16 lanes: lanes differing in bit 0, bit 1, a
+// mirror of 8 (bit 2, once bits 0 and 1 agree) and of 16 lanes (bit 3).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(uint32_t, v)));
+}
+
+template <class T, class Op>
+__device__ __forceinline__ T wave_reduce(T v, Op op) {
+  v = op(v, dpp<kXor1>(v));
+  v = op(v, dpp<kXor2>(v));
+  v = op(v, dpp<kMirror8>(v));
+  v = op(v, dpp<kMirror16>(v));
+  v = op(v, __shfl_xor(v, 16));
+  return op(v, __shfl_xor(v, 32));
+}
+
+// Two sets of one value for each wave, used in turn: whoever writes a set has
+// passed the barrier of the reduction between, which every wave reaches after
+// reading that set. So one barrier a reduction is enough.
+struct Buffers {
+  double v[2][16];
+};
+
 template <int TPR, class T, class Op>
-__device__ __forceinline__ T row_reduce(T v, Op op, T (&buf)[16]) {
-  for (int m = 32; m > 0; m >>= 1) v = op(v, __shfl_xor(v, m));
+__device__ __forceinline__ T row_reduce(T v, Op op, Buffers& b, int& turn) {
+  v = wave_reduce(v, op);
   if constexpr (TPR > 64) {
-    __syncthreads();  // a reduction before has read the buffer
-    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+    T* set = (T*)b.v[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) set[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = buf[0];
+    v = set[0];
 #pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) v = op(v, buf[w]);
+    for (int w = 1; w < TPR / 64; ++w) v = op(v, set[w]);
   }
   return v;
 }
 
-struct Buffers {
-  double sum[16];
-  float amax[16];
-  uint32_t hw[16], lw[16];
-};
-
 template <int TPR>
-__device__ __forceinline__ double row_sum(double v, Buffers& b) {
-  return row_reduce<TPR>(v, [](double x, double y) { return x + y; }, b.sum);
+__device__ __forceinline__ double row_sum(double v, Buffers& b, int& turn) {
+  return row_reduce<TPR>(v, [](double x, double y) { return x + y; }, b, turn);
 }
 
+__device__ __forceinline__ float max_f32(float a, float b) { return fmaxf(a, b); }
+
 // ------------------------------------------------------------------ the end of a row
+// The larger of both halves of a pair's magnitudes.
+__device__ __forceinline__ uint32_t halves_max(uint32_t v) { return max(v & 0xFFFFu, v >> 16); }
+
+// The largest magnitude of eight values that is no NaN.
+__device__ __forceinline__ float amax8(const Raw8<false>& o) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(o[j]));
+  return m;
+}
+
+__device__ __forceinline__ uint32_t abs_max8(const Raw8<false>& o) {
+  uint32_t m = o.d[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int d = 1; d < 4; ++d) m = pk_max_u16(m, o.d[d] & 0x7FFF7FFFu);
+  return m;
+}
+
+// The codes of qdg_quantize_act's int8 rule for a finite row: rne(f * inv) of
+// the rounded product is the low byte of product + 1.5 * 2^23, and no product
+// is above 127 (1 + 2^-23).
+__device__ __forceinline__ u32x2_t encode_int8x8_finite(const Raw8<false>& o, float inv) {
+  uint32_t c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float p = o[j] * inv;
+    asm volatile("" : "+v"(p));  // two roundings: not one fused product and sum
+    c[j] = __builtin_bit_cast(uint32_t, p + 12582912.f);
+  }
+  u32x2_t out;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(c[4 * h + 1], c[4 * h], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(c[4 * h + 3], c[4 * h + 2], 0x04000C0Cu);
+    out[h] = lo | hi;
+  }
+  return out;
+}
+
 // The bf16 values o of a row (chunk c of thread t: values 8 (c TPR + t) and on;
 // 0 behind the end) as rows and codes.
 template <int TPR, int CH>
 __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, int64_t row, int t, const RowOut& out,
-                                           Buffers& buf) {
+                                           Buffers& buf, int& turn) {
   if (out.rows) {
     uint16_t* p = out.rows + row * out.ld;
 #pragma unroll
@@ -138,15 +291,6 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
   }
   if (out.quant == QDG_Q_NONE) return;
   uint8_t* q = out.qa + row * out.ldq;
-  auto store_codes = [&](int i, u32x2_t v) {
-    if (i + 8 <= n) {
-      *(u32x2_t*)(q + i) = v;  // qa and its stride are multiples of 16 bytes
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + j < n) q[i + j] = (uint8_t)((j < 4 ? v.x : v.y) >> (8 * (j & 3)));
-    }
-  };
   if (out.quant == QDG_Q_INT8_ZP) {
     uint32_t pos = 0, neg = 0;  // packed maxima
 #pragma unroll
@@ -156,16 +300,17 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
         pos = pk_max_i16(pos, o[c].d[d]);
         neg = pk_max_u16(neg, o[c].d[d]);
       }
-    uint32_t hw = max(pos & 0xFFFFu, pos >> 16), lw = max(neg & 0xFFFFu, neg >> 16);
-    auto most = [](uint32_t x, uint32_t y) { return max(x, y); };
-    hw = row_reduce<TPR>(hw, most, buf.hw);
-    lw = row_reduce<TPR>(lw, most, buf.lw);
+    uint32_t hw = halves_max(pos), lw = halves_max(neg);
+    uint32_t both = row_reduce<TPR>(hw | lw << 16, pk_max_u16, buf, turn);
+    hw = both & 0xFFFFu;
+    lw = both >> 16;
     if (hw >= 0x7F80u || lw >= 0xFF80u) {  // an infinity or a NaN: they do not count
       hw = lw = 0;
 #pragma unroll
       for (int c = 0; c < CH; ++c) zp_finite_max<4>(o[c].d, hw, lw);
-      hw = row_reduce<TPR>(hw, most, buf.hw);
-      lw = row_reduce<TPR>(lw, most, buf.lw);
+      both = row_reduce<TPR>(hw | lw << 16, pk_max_u16, buf, turn);
+      hw = both & 0xFFFFu;
+      lw = both >> 16;
     }
     const ZpRow z = zp_row(lw >= 0x8000u ? bf16_to_f32(lw) : 0.f, bf16_to_f32(hw));
     if (t == 0) {
@@ -177,32 +322,40 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
       if ((c * TPR + t) * 8 < n) {
         uint32_t code[2];
         encode_zp<4>(o[c].d, z, code);
-        store_codes((c * TPR + t) * 8, u32x2_t{code[0], code[1]});
+        store_codes(q, (c * TPR + t) * 8, n, u32x2_t{code[0], code[1]});
       }
     return;
   }
-  float amax[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    amax[c] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax[c] = fmaxf(amax[c], fabsf(o[c][j]));
-  }
   if (out.quant == QDG_Q_INT8) {
-    float m = 0.f;
+    uint32_t word = 0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) m = fmaxf(m, amax[c]);
-    m = row_reduce<TPR>(m, [](float x, float y) { return fmaxf(x, y); }, buf.amax);
+    for (int c = 0; c < CH; ++c) word = pk_max_u16(word, abs_max8(o[c]));
+    word = row_reduce<TPR>(halves_max(word), [](uint32_t x, uint32_t y) { return max(x, y); }, buf, turn);
+    const bool finite = word < 0x7F80u;
+    float m = bf16_to_f32(word);
+    if (!finite) {  // a NaN does not count
+      m = 0.f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) m = fmaxf(m, amax8(o[c]));
+      m = row_reduce<TPR>(m, max_f32, buf, turn);
+    }
     const bool nz = m > 0.f;
     const float inv = nz ? __fdiv_rn(127.0f, m) : 0.f;
     if (t == 0) ((float*)out.scales)[row] = nz ? __fdiv_rn(m, 127.0f) : 1.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
       if ((c * TPR + t) * 8 < n) {
-        float f[8];
+        u32x2_t code;
+        // a row that is smaller than the quotient's range (inv infinite) takes the general way too
+        if (finite && inv < 0x1p127f) {
+          code = encode_int8x8_finite(o[c], inv);
+        } else {
+          float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = o[c][j];
-        store_codes((c * TPR + t) * 8, encode_int8x8(f, inv));
+          for (int j = 0; j < 8; ++j) f[j] = o[c][j];
+          code = encode_int8x8(f, inv);
+        }
+        store_codes(q, (c * TPR + t) * 8, n, code);
       }
     return;
   }
@@ -211,12 +364,23 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
   const bool fp8 = out.quant == QDG_Q_FP8E4M3;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    float m = amax[c];
-    m = fmaxf(m, __shfl_xor(m, 1));
-    m = fmaxf(m, __shfl_xor(m, 2));
+    uint32_t word = abs_max8(o[c]);
+    word = pk_max_u16(word, dpp<kXor1>(word));
+    word = pk_max_u16(word, dpp<kXor2>(word));
     if (fp8) {
-      m = fmaxf(m, __shfl_xor(m, 4));
-      m = fmaxf(m, __shfl_xor(m, 8));
+      word = pk_max_u16(word, dpp<kMirror8>(word));
+      word = pk_max_u16(word, dpp<kMirror16>(word));
+    }
+    word = halves_max(word);
+    float m = bf16_to_f32(word);
+    if (__any(word > 0x7F80u)) {  // a NaN does not count
+      m = amax8(o[c]);
+      m = fmaxf(m, dpp<kXor1>(m));
+      m = fmaxf(m, dpp<kXor2>(m));
+      if (fp8) {
+        m = fmaxf(m, dpp<kMirror8>(m));
+        m = fmaxf(m, dpp<kMirror16>(m));
+      }
     }
     const int i = (c * TPR + t) * 8;
     if (i >= n) continue;
@@ -235,106 +399,223 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
   }
 }
 
+// ------------------------------------------------------------------ doubt
+// Between binary64 values: their chains side by side would take the registers
+// that let another wave in.
+__device__ __forceinline__ void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }
+
+// y is a binary32 value with an error of at most ULPS units in its last place:
+// near enough to the middle of two bf16 numbers (low half 0x8000) it leaves the
+// rounding open. 0 to 2 ULPS (in the high half) there, more elsewhere.
+template <int ULPS>
+__device__ __forceinline__ uint32_t to_middle(float y) {
+  return (__builtin_bit_cast(uint32_t, y) << 16) + ((0x8000u + ULPS) << 16);
+}
+template <int ULPS>
+constexpr uint32_t kMiddle = (uint32_t)(2 * ULPS) << 16 | 0xFFFFu;
+
 // ------------------------------------------------------------------ norms
 // 1 / sqrt(mean of squares + eps) of the row v, and with LAYER its mean.
-template <int TPR, int CH>
-__device__ __forceinline__ void row_stats(const float (&v)[CH][8], int n, int t, bool layer, float eps, double& mean,
-                                          double& rs, Buffers& buf) {
+template <int TPR, int CH, bool F32>
+__device__ __forceinline__ void row_stats(Raw8<F32> (&v)[CH], int n, int t, bool layer, float eps, double& mean,
+                                          double& rs, Buffers& buf, int& turn) {
   mean = 0.0;
+  double s = 0.0;
   if (layer) {
-    double s = 0.0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+    for (int c = 0; c < CH; ++c) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += (double)v[c][j];
-    mean = row_sum<TPR>(s, buf) / (double)n;
-  }
-  double s = 0.0;
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double d = (double)v[c][j] - mean;
-      if ((c * TPR + t) * 8 + j < n) s += d * d;
+      v[c].renew();
     }
-  rs = 1.0 / sqrt(row_sum<TPR>(s, buf) / (double)n + (double)eps);
+    mean = row_sum<TPR>(s, buf, turn) / (double)n;
+    s = 0.0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int rest = n - (c * TPR + t) * 8;  // the zeros behind the end do not count
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double d = j < rest ? (double)v[c][j] - mean : 0.0;
+        s = __builtin_fma(d, d, s);
+        one_at_a_time();
+      }
+      v[c].renew();
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double d = (double)v[c][j];
+        s = __builtin_fma(d, d, s);
+      }
+      v[c].renew();
+    }
+  }
+  rs = 1.0 / sqrt(row_sum<TPR>(s, buf, turn) / (double)n + (double)eps);
 }
 
-template <int TPR, int CH, bool XF, bool RF>
+// What is absent is neutral: a factor 1, a term -0 (which leaves a sum its sign).
+// The new stream of eight values: residual_scale * r + gate * t. PLAIN: the
+// product has at most 16 significant bits, the sum one rounding.
+template <bool PLAIN, bool XF, bool RF>
+__device__ __forceinline__ Raw8<RF> join8(const NormArgs& a, const Raw8<XF>& x, const Raw8<RF>& r, const void* gate, int i,
+                                          double mean, double rs) {
+  const int n = a.n;
+  const float scale = a.residual ? a.residual_scale : -1.0f;  // of zeros
+  float v[8];
+  const Vec8 g = load_vec8(gate, 1.0f, !PLAIN && a.wf32, i, n);
+  if constexpr (PLAIN) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(scale, r[j], x[j] * g.v[j]);
+  } else {
+    const Vec8 w = load_vec8(a.post_weight, 1.0f, a.wf32, i, n), b = load_vec8(a.post_bias, -0.0f, a.wf32, i, n);
+    const double offset = a.post_weight ? (double)a.weight_offset : 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      double d = ((double)x[j] - mean) * rs * ((double)w.v[j] + offset) + (double)b.v[j];
+      d = __builtin_fma((double)scale, (double)r[j], d * (double)g.v[j]);
+      v[j] = (float)d;
+      one_at_a_time();
+    }
+    const int rest = n - i;
+    if (rest < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < rest ? v[j] : 0.f;
+    }
+  }
+  Raw8<RF> s;
+  if constexpr (RF) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s.d[j] = __builtin_bit_cast(uint32_t, v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s.d[j] = to_bf16_pair(v[2 * j], v[2 * j + 1]);
+  }
+  return s;
+}
+
+// Eight normed values. q = rs * w and y = s * q carry four roundings of 2^-24
+// (rs, w + offset, both products): 4 units in the last place of y, 6 are
+// allowed for. Not PLAIN (a bias or a mean): y = m + b, with m's error, the
+// rounding of s - mean and its own one within 2^-21 |m| + 2^-23 |b|; the
+// roundings of both ends of that interval are compared. Rows and weights whose
+// products leave the middle of binary32's range are computed in binary64.
+template <bool PLAIN, bool RF>
+__device__ __forceinline__ Raw8<false> norm8(const NormArgs& a, const Raw8<RF>& s, const Vec8& w, const Vec8& b, int i,
+                                             double mean, double rs, bool in_range) {
+  Raw8<false> o;
+  const float rs32 = (float)rs, offset = a.weight ? a.weight_offset : 0.f;
+  bool doubt = !in_range;
+  float q[8], q_most = 0.f, q_least = __builtin_inff();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    q[j] = rs32 * (w.v[j] + offset);
+    q_most = fmaxf(q_most, fabsf(q[j]));
+    q_least = fminf(q_least, fabsf(q[j]));
+  }
+  doubt |= !(q_least > 0x1p-100f) || !(q_most < 0x1p100f);
+  if constexpr (PLAIN) {
+    uint32_t near = ~0u;
+    float y[8], least = __builtin_inff();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      y[j] = s[j] * q[j];
+      near = min(near, to_middle<6>(y[j]));
+      least = fminf(least, fabsf(y[j]));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o.d[j] = to_bf16_pair(y[2 * j], y[2 * j + 1]);
+    doubt |= near <= kMiddle<6> || !(least > 0x1p-100f);
+  } else {
+    uint32_t differ = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo[2], hi[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float m = (float)((double)s[2 * j + h] - mean) * q[2 * j + h], bj = b.v[2 * j + h], sum = m + bj;
+        const float e = __builtin_fmaf(fabsf(m), 0x1p-21f, __builtin_fmaf(fabsf(bj), 0x1p-23f, 0x1p-110f));
+        lo[h] = sum - e;
+        hi[h] = sum + e;
+      }
+      o.d[j] = to_bf16_pair(lo[0], lo[1]);
+      differ |= o.d[j] ^ to_bf16_pair(hi[0], hi[1]);
+      one_at_a_time();
+    }
+    doubt |= differ != 0;
+  }
+  if (doubt) {
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      double d = (PLAIN ? (double)s[j] : (double)s[j] - mean) * rs * ((double)w.v[j] + (double)offset);
+      if (!PLAIN) d += (double)b.v[j];
+      z[j] = (float)d;
+      one_at_a_time();
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o.d[j] = to_bf16_pair(z[2 * j], z[2 * j + 1]);
+  }
+  const int rest = a.n - i;
+  if (rest < 8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o.d[j] &= 2 * j + 1 < rest ? ~0u : 2 * j < rest ? 0xFFFFu : 0u;
+  }
+  return o;
+}
+
+template <int TPR, int CH, bool XF, bool RF, bool PLAIN>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
   __shared__ Buffers buf;
+  int turn = 0;
   constexpr int kThreads = TPR < 256 ? 256 : TPR, RPB = kThreads / TPR;
   const int t = threadIdx.x % TPR, n = a.n;
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.M; r0 += (int64_t)gridDim.x * RPB) {
     const int64_t row = r0 + threadIdx.x / TPR;
     if (TPR < 256 && row >= a.M) break;  // whole waves: no barrier below
-    const void* x = (const char*)a.x + row * a.ldx * (XF ? 4 : 2);
-    const void* r = a.residual ? (const char*)a.residual + row * a.ldr * (RF ? 4 : 2) : nullptr;
-    const void* g = a.gate ? (const char*)a.gate + row * a.ldg * (a.wf32 ? 4 : 2) : nullptr;
-    float v[CH][8];
+    const char* x = (const char*)a.x + row * a.ldx * (XF ? 4 : 2);
+    const char* r = (const char*)a.residual + row * a.ldr * (RF ? 4 : 2);
+    const char* g = a.gate ? (const char*)a.gate + row * a.ldg * (a.wf32 ? 4 : 2) : nullptr;
+    Raw8<XF> v[CH];
+    Raw8<RF> s[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const Raw8<XF> w = load8<XF>(x, (c * TPR + t) * 8, n);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = w[j];
+      v[c] = {};
+      s[c] = {};
+      const int i = (c * TPR + t) * 8;
+      if (i < n) {
+        v[c] = load8<XF>(x, i, n);
+        if (a.residual) s[c] = load8<RF>(r, i, n);
+      }
     }
     double mean = 0.0, rs = 1.0;
-    if (a.post_norm) row_stats<TPR, CH>(v, n, t, a.layer, a.eps, mean, rs, buf);
+    if (!PLAIN && a.post_norm) row_stats<TPR, CH, XF>(v, n, t, a.layer, a.eps, mean, rs, buf, turn);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (c * TPR + t) * 8;
-      Raw8<RF> w = {}, s;
-      if (r) w = load8<RF>(r, i, n);
-      float pw[8], pb[8], gw[8];
-      if (a.post_weight) load_vec8(a.post_weight, a.wf32, i, n, pw);
-      if (a.post_bias) load_vec8(a.post_bias, a.wf32, i, n, pb);
-      if (g) load_vec8(g, a.wf32, i, n, gw);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        double d = (double)v[c][j];
-        if (a.post_norm) {
-          d = (d - mean) * rs;
-          if (a.post_weight) d *= (double)pw[j] + (double)a.weight_offset;
-          if (a.post_bias) d += (double)pb[j];
-        }
-        if (g) d *= (double)gw[j];
-        if (r) d += (double)a.residual_scale * (double)w[j];
-        v[c][j] = i + j < n ? (float)d : 0.f;
+      if (i < n) {
+        s[c] = join8<PLAIN, XF, RF>(a, v[c], s[c], g, i, mean, rs);
+        if (a.residual_out) store8<RF>((char*)a.residual_out + row * a.lds * (RF ? 4 : 2), i, n, s[c]);
       }
-      if constexpr (RF) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s.d[j] = __builtin_bit_cast(uint32_t, v[c][j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s.d[j] = to_bf16_pair(v[c][2 * j], v[c][2 * j + 1]);
-          v[c][2 * j] = s[2 * j];
-          v[c][2 * j + 1] = s[2 * j + 1];
-        }
-      }
-      if (a.residual_out && i < n) store8<RF>((char*)a.residual_out + row * a.lds * (RF ? 4 : 2), i, n, s);
+      s[c].renew();
     }
     if (!a.out.rows && a.out.quant == QDG_Q_NONE) continue;
-    row_stats<TPR, CH>(v, n, t, a.layer, a.eps, mean, rs, buf);
+    row_stats<TPR, CH, RF>(s, n, t, !PLAIN && a.layer, a.eps, mean, rs, buf, turn);
+    const bool in_range = rs > 0x1p-60 && rs < 0x1p60;
     Raw8<false> o[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (c * TPR + t) * 8;
-      float wt[8], bs[8];
-      if (a.weight) load_vec8(a.weight, a.wf32, i, n, wt);
-      if (a.bias) load_vec8(a.bias, a.wf32, i, n, bs);
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        double d = ((double)v[c][j] - mean) * rs;
-        if (a.weight) d *= (double)wt[j] + (double)a.weight_offset;
-        if (a.bias) d += (double)bs[j];
-        y[j] = i + j < n ? (float)d : 0.f;
+      o[c] = {};
+      if (i < n) {
+        const Vec8 w = load_vec8(a.weight, 1.0f, !PLAIN && a.wf32, i, n);
+        const Vec8 b = load_vec8(PLAIN ? nullptr : a.bias, -0.0f, a.wf32, i, n);
+        o[c] = norm8<PLAIN, RF>(a, s[c], w, b, i, mean, rs, in_range);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[c].d[j] = to_bf16_pair(y[2 * j], y[2 * j + 1]);
+      o[c].renew();
     }
-    finish_row<TPR, CH>(o, n, row, t, a.out, buf);
+    finish_row<TPR, CH>(o, n, row, t, a.out, buf, turn);
   }
 }
 
@@ -347,27 +628,88 @@ __device__ __forceinline__ double act64(double g, int act) {
   return g / (1.0 + exp(-z));
 }
 
+// act(g) * u of eight values. In binary32: e = 2^t (1 + r ln 2), t = -g log2(e)
+// rounded and r what that left out (within 2^-24 |t| 2^-24 and a rounding), so
+// that e is within 2 units in its last place (v_exp_f32 has one) and a rounding;
+// 1 + e, its reciprocal (one unit) and two products follow: at most 9 units in
+// the last place, 11 are allowed for. GELU's t = -g (c1 + c3 g^2) is itself off
+// by up to 2.5 roundings and those of its constants, 4 2^-24 |t|, which the
+// exponential turns into as much times ln 2 of its value: within 2^-24 (22 + 4 |t|)
+// all told, and both ends of that interval are compared. Values below 2^-100 are
+// computed in binary64.
+template <bool YF>
+__device__ __forceinline__ Raw8<false> gated8(const Raw8<YF>& g, const Raw8<YF>& u, int act) {
+  Raw8<false> o;
+  float y[8];
+  uint32_t open = 0;  // values whose bf16 number is open
+  if (act == QDG_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      constexpr float kL = 1.44269504f, kLo = 1.92596303e-8f, kLn2 = 0.69314718f;  // log2(e) = kL + kLo
+      const float h = __builtin_amdgcn_fmed3f(g[j], -128.f, 128.f);
+      const float t = -h * kL, r = __builtin_fmaf(-h, kLo, __builtin_fmaf(-h, kL, -t));
+      const float p = __builtin_amdgcn_exp2f(t);
+      const float e = __builtin_fmaf(p, r * kLn2, p);
+      y[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + e) * u[j];
+      open |= to_middle<11>(y[j]) <= kMiddle<11> || !(fabsf(y[j]) > 0x1p-100f) ? 1u << j : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o.d[j] = to_bf16_pair(y[2 * j], y[2 * j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      constexpr float kC1 = -2.3022082f, kC3 = -0.10294324f;  // -2 sqrt(2 / pi) log2(e), and 0.044715 of it
+      const float h = __builtin_amdgcn_fmed3f(g[j], -32.f, 32.f);
+      const float t = h * __builtin_fmaf(h * h, kC3, kC1);
+      const float e = __builtin_amdgcn_exp2f(t);
+      y[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + e) * u[j];
+      const float off = __builtin_fmaf(fabsf(t), 0x1p-22f, 22 * 0x1p-24f) * y[j];
+      const uint32_t both = to_bf16_pair(y[j] - off, y[j] + off);
+      open |= (both & 0xFFFFu) != both >> 16 || !(fabsf(y[j]) > 0x1p-100f) ? 1u << j : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o.d[j] = to_bf16_pair(y[2 * j], y[2 * j + 1]);
+  }
+  if (open) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (open >> j & 1) {
+        const uint32_t b = to_bf16_pair((float)(act64((double)g[j], act) * (double)u[j]), 0.f);
+        o.d[j >> 1] = j & 1 ? (o.d[j >> 1] & 0xFFFFu) | b << 16 : (o.d[j >> 1] & 0xFFFF0000u) | (b & 0xFFFFu);
+        one_at_a_time();
+      }
+  }
+  return o;
+}
+
 template <int TPR, int CH, bool YF>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_kernel(GatedArgs a) {
   __shared__ Buffers buf;
+  int turn = 0;
   constexpr int kThreads = TPR < 256 ? 256 : TPR, RPB = kThreads / TPR;
   const int t = threadIdx.x % TPR, n = a.n;
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.M; r0 += (int64_t)gridDim.x * RPB) {
     const int64_t row = r0 + threadIdx.x / TPR;
     if (TPR < 256 && row >= a.M) break;  // whole waves: no barrier below
     const char* y = (const char*)a.y + row * a.ldy * (YF ? 4 : 2);
-    Raw8<false> o[CH];
+    Raw8<YF> g[CH], u[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (c * TPR + t) * 8;
-      const Raw8<YF> g = load8<YF>(y, i, n), u = load8<YF>(y + (int64_t)n * (YF ? 4 : 2), i, n);
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = (float)(act64((double)g[j], a.act) * (double)u[j]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[c].d[j] = to_bf16_pair(f[2 * j], f[2 * j + 1]);
+      g[c] = u[c] = {};
+      if (i < n) {
+        g[c] = load8<YF>(y, i, n);
+        u[c] = load8<YF>(y + (int64_t)n * (YF ? 4 : 2), i, n);
+      }
     }
-    finish_row<TPR, CH>(o, n, row, t, a.out, buf);
+    Raw8<false> o[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      o[c] = {};
+      if ((c * TPR + t) * 8 < n) o[c] = gated8<YF>(g[c], u[c], a.act);
+      o[c].renew();
+    }
+    finish_row<TPR, CH>(o, n, row, t, a.out, buf, turn);
   }
 }
 
@@ -381,14 +723,23 @@ hipError_t go(K kernel, int threads, int rows_per_block, const A& a, hipStream_t
   return hipGetLastError();
 }
 
-template <bool XF, bool RF>
+// PLAIN: an RMS norm of the stream with bf16 weights, no bias, and a join that
+// one rounding of binary32 settles; the rest keeps its registers.
+template <bool XF, bool RF, bool PLAIN>
 hipError_t norm_shape(const NormArgs& a, hipStream_t s) {
-  if (a.n <= 512) return go(norm_kernel<64, 1, XF, RF>, 256, 4, a, s);
-  if (a.n <= 2048) return go(norm_kernel<256, 1, XF, RF>, 256, 1, a, s);
-  if (a.n <= 4096) return go(norm_kernel<256, 2, XF, RF>, 256, 1, a, s);
-  if (a.n <= 8192) return go(norm_kernel<256, 4, XF, RF>, 256, 1, a, s);
-  if (a.n <= 16384) return go(norm_kernel<512, 4, XF, RF>, 512, 1, a, s);
-  return go(norm_kernel<1024, 4, XF, RF>, 1024, 1, a, s);
+  constexpr int kCh = PLAIN ? 2 : 1;  // up to 8192 values
+  if (a.n <= 512) return go(norm_kernel<64, 1, XF, RF, PLAIN>, 256, 4, a, s);
+  if (a.n <= 2048) return go(norm_kernel<256, 1, XF, RF, PLAIN>, 256, 1, a, s);
+  if (a.n <= 4096) return go(norm_kernel<512 / kCh, kCh, XF, RF, PLAIN>, 512 / kCh, 1, a, s);
+  if (a.n <= 8192) return go(norm_kernel<1024 / kCh, kCh, XF, RF, PLAIN>, 1024 / kCh, 1, a, s);
+  if (a.n <= 16384) return go(norm_kernel<1024, 2, XF, RF, PLAIN>, 1024, 1, a, s);
+  return go(norm_kernel<1024, 4, XF, RF, PLAIN>, 1024, 1, a, s);
+}
+
+template <bool XF, bool RF>
+hipError_t norm_kind(const NormArgs& a, hipStream_t s) {
+  const bool plain = !a.post_norm && !a.layer && !a.bias && !a.wf32 && !(XF && a.gate);
+  return plain ? norm_shape<XF, RF, true>(a, s) : norm_shape<XF, RF, false>(a, s);
 }
 
 template <bool YF>
@@ -396,8 +747,8 @@ hipError_t gated_shape(const GatedArgs& a, hipStream_t s) {
   if (a.n <= 512) return go(gated_kernel<64, 1, YF>, 256, 4, a, s);
   if (a.n <= 2048) return go(gated_kernel<256, 1, YF>, 256, 1, a, s);
   if (a.n <= 4096) return go(gated_kernel<256, 2, YF>, 256, 1, a, s);
-  if (a.n <= 8192) return go(gated_kernel<256, 4, YF>, 256, 1, a, s);
-  if (a.n <= 16384) return go(gated_kernel<512, 4, YF>, 512, 1, a, s);
+  if (a.n <= 8192) return go(gated_kernel<512, 2, YF>, 512, 1, a, s);
+  if (a.n <= 16384) return go(gated_kernel<1024, 2, YF>, 1024, 1, a, s);
   if (a.n <= 32768) return go(gated_kernel<1024, 4, YF>, 1024, 1, a, s);
   return go(gated_kernel<1024, 8, YF>, 1024, 1, a, s);
 }
@@ -405,8 +756,8 @@ hipError_t gated_shape(const GatedArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, bool xf32, bool rf32, hipStream_t s) {
-  if (xf32) return rf32 ? norm_shape<true, true>(a, s) : norm_shape<true, false>(a, s);
-  return rf32 ? norm_shape<false, true>(a, s) : norm_shape<false, false>(a, s);
+  if (xf32) return rf32 ? norm_kind<true, true>(a, s) : norm_kind<true, false>(a, s);
+  return rf32 ? norm_kind<false, true>(a, s) : norm_kind<false, false>(a, s);
 }
 
 hipError_t launch_gated_act(const GatedArgs& a, bool yf32, hipStream_t s) {
