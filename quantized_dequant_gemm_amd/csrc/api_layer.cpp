@@ -98,7 +98,7 @@ qdg_status check_lora(const qdg_lora_config* c, int64_t M, int32_t block_m) {
 // Bytes of the inner sums of `blocks` blocks.
 int64_t lora_bytes(const qdg_lora_config* c, int64_t blocks, int32_t block_m) {
   const int cols = c->num_slices * lora_rank_pad(c->rank);
-  return lora_split(blocks * (block_m / 16), cols, c->k) * blocks * block_m * cols * (int64_t)sizeof(float);
+  return lora_split(blocks * (block_m / 16), block_m, cols, c->k) * blocks * block_m * cols * (int64_t)sizeof(float);
 }
 
 }  // namespace
@@ -197,7 +197,7 @@ qdg_status qdg_lora_workspace(const qdg_lora_config* cfg, int64_t M, int32_t blo
   const qdg_status st = check_lora(cfg, M, block_m);
   if (st != QDG_OK) return st;
   if (!bytes) return fail(QDG_ERR_INVALID_ARG, "bytes is NULL");
-  // fewer blocks may be split where many are not; from 512 tiles on none is
+  // fewer blocks may be split where many are not; from 512 blocks on none is
   int64_t most = 0;
   const int64_t blocks = M > 0 ? lora_blocks(M, cfg->num_adapters, block_m) : 0;
   for (int64_t b = 1; b <= blocks && b <= 512; ++b) {
@@ -251,7 +251,7 @@ qdg_status qdg_lora(const qdg_lora_config* cfg, const void* X, const void* A, co
   a.rank_pad = lora_rank_pad(cfg->rank);
   for (int i = 0; i < cfg->num_slices; ++i) a.slice_end[i] = (int)cfg->slice_end[i];
   a.block_m = block_m;
-  a.split = lora_split((int64_t)a.blocks * (block_m / 16), a.num_slices * a.rank_pad, cfg->k);
+  a.split = lora_split((int64_t)a.blocks * (block_m / 16), block_m, a.num_slices * a.rank_pad, cfg->k);
   a.yf32 = cfg->otype == QDG_O_F32;
   const hipError_t e = launch_lora(a, (hipStream_t)stream);
   if (e == hipErrorInvalidConfiguration)

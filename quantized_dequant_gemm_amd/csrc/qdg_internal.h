@@ -248,7 +248,7 @@ struct LoraArgs {
   const int32_t* block_adapter;
   const int32_t* num_padded;
   void* Y;
-  float* partial;          // [split][rows in order][slices * rank_pad]
+  float* partial;          // [split][16-row tiles][slices * rank_pad / 16][64][4]
   int64_t ldx, ldy;
   int64_t M;
   int n, k;
@@ -261,8 +261,7 @@ struct LoraArgs {
 // The most blocks of block_m rows that M rows of at most E adapters make.
 int64_t lora_blocks(int64_t M, int64_t E, int block_m);
 int lora_rank_pad(int rank);
-int lora_split(int64_t tiles, int columns, int64_t k);
-int64_t lora_expand_units(const LoraArgs& a);
+int lora_split(int64_t tiles, int block_m, int columns, int64_t k);
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
 
 #endif
