@@ -760,7 +760,7 @@ qdg_status qdg_gated_act(const qdg_gated_config* cfg, const void* Y, int64_t M, 
    significand (2^-18 of their value); the sum joins Y in binary32 and is
    rounded once to otype. Results do not depend on other rows' values, but their
    last bits may on M and the grouping (the order of the inner sums).
-   n, k in [1, 2^26]; rank 1..256; num_slices 1..4, slice_end ascending, the
+   n, k in [1, 2^20]; rank 1..256; num_slices 1..4, slice_end ascending, the
    last one n; num_adapters 1..1024; M in [0, 2^20] (0 enqueues nothing);
    block_m 16, 32, 64 or 128: the smaller while adapters hold few rows each
    (about 32 rows an adapter: 16 up to there, 64 beyond). */

@@ -34,7 +34,7 @@ size_t size_of(int32_t type) { return type == QDG_O_F32 ? 4 : 2; }
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
 constexpr int64_t kMaxStride = (int64_t)1 << 31;
 constexpr int64_t kMaxNorm = 32768, kMaxGated = 65536;
-constexpr int64_t kMaxSide = (int64_t)1 << 26;
+constexpr int64_t kMaxSide = (int64_t)1 << 20;
 constexpr int64_t kMaxLoraRows = (int64_t)1 << 20;
 
 bool bad_stride(int64_t ld, int64_t n) { return ld < n || ld > kMaxStride; }
@@ -79,7 +79,7 @@ qdg_status check_lora(const qdg_lora_config* c, int64_t M, int32_t block_m) {
   if (!c) return fail(QDG_ERR_INVALID_ARG, "config is NULL");
   if (c->n < 1 || c->k < 1 || c->rank < 1 || c->num_adapters < 1 || c->num_slices < 1)
     return fail(QDG_ERR_INVALID_ARG, "n, k, rank, num_adapters and num_slices must be positive");
-  if (c->n > kMaxSide || c->k > kMaxSide) return fail(QDG_ERR_UNSUPPORTED, "n and k must be at most 2^26");
+  if (c->n > kMaxSide || c->k > kMaxSide) return fail(QDG_ERR_UNSUPPORTED, "n and k must be at most 2^20");
   if (c->rank > 256) return fail(QDG_ERR_UNSUPPORTED, "rank must be at most 256");
   if (c->num_adapters > 1024) return fail(QDG_ERR_UNSUPPORTED, "at most 1024 adapters");
   if (c->num_slices > 4) return fail(QDG_ERR_UNSUPPORTED, "at most 4 slices");
@@ -95,10 +95,28 @@ qdg_status check_lora(const qdg_lora_config* c, int64_t M, int32_t block_m) {
   return check_block_m(block_m);
 }
 
-// Bytes of the inner sums of `blocks` blocks.
-int64_t lora_bytes(const qdg_lora_config* c, int64_t blocks, int32_t block_m) {
-  const int cols = c->num_slices * lora_rank_pad(c->rank);
-  return lora_split(blocks * (block_m / 16), block_m, cols, c->k) * blocks * block_m * cols * (int64_t)sizeof(float);
+// The geometry of a call whose rows make up to `blocks` blocks, and what runs it.
+LoraArgs lora_geometry(const qdg_lora_config* c, int64_t blocks, int32_t block_m) {
+  LoraArgs a = {};
+  a.ldx = c->ldx;
+  a.ldy = c->ldy;
+  a.n = (int)c->n;
+  a.k = (int)c->k;
+  a.num_adapters = c->num_adapters;
+  a.num_slices = c->num_slices;
+  a.rank = c->rank;
+  for (int i = 0; i < c->num_slices; ++i) a.slice_end[i] = (int)c->slice_end[i];
+  a.block_m = block_m;
+  a.block_shift = block_m == 16 ? 0 : block_m == 32 ? 1 : block_m == 64 ? 2 : 3;
+  a.blocks = (int)blocks;
+  a.yf32 = c->otype == QDG_O_F32;
+  lora_choose(&a);
+  return a;
+}
+
+// Bytes of the inner sums.
+int64_t lora_bytes(const LoraArgs& a) {
+  return a.fused ? 0 : (int64_t)a.split * a.blocks * a.block_m * a.num_slices * a.rank_pad * (int64_t)sizeof(float);
 }
 
 }  // namespace
@@ -200,12 +218,9 @@ qdg_status qdg_lora_workspace(const qdg_lora_config* cfg, int64_t M, int32_t blo
   // fewer blocks may be split where many are not; from 512 blocks on none is
   int64_t most = 0;
   const int64_t blocks = M > 0 ? lora_blocks(M, cfg->num_adapters, block_m) : 0;
-  for (int64_t b = 1; b <= blocks && b <= 512; ++b) {
-    const int64_t need = lora_bytes(cfg, b, block_m);
-    most = need > most ? need : most;
-  }
-  if (blocks > 0) {
-    const int64_t need = lora_bytes(cfg, blocks, block_m);
+  for (int64_t b = 1; b <= blocks; ++b) {
+    if (b == 513) b = blocks;
+    const int64_t need = lora_bytes(lora_geometry(cfg, b, block_m));
     most = need > most ? need : most;
   }
   *bytes = (size_t)most;
@@ -224,15 +239,17 @@ qdg_status qdg_lora(const qdg_lora_config* cfg, const void* X, const void* A, co
   if (!aligned(X, 2) || !aligned(A, 2) || !aligned(B, 2) || !aligned(Y, size_of(cfg->otype)) || !aligned(ranks, 4) ||
       !aligned(scales, 4) || !aligned(sorted_ids, 4) || !aligned(block_adapter, 4) || !aligned(num_padded, 4))
     return fail(QDG_ERR_MISALIGNED, "pointers must be aligned to their elements");
-  LoraArgs a = {};
-  a.blocks = (int)lora_blocks(M, cfg->num_adapters, block_m);
-  const size_t need = (size_t)lora_bytes(cfg, a.blocks, block_m);
-  if (!workspace || ws_bytes < need)
+  LoraArgs a = lora_geometry(cfg, lora_blocks(M, cfg->num_adapters, block_m), block_m);
+  const size_t need = (size_t)lora_bytes(a);
+  if (need > 0 && (!workspace || ws_bytes < need))
     return fail(QDG_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace ? ws_bytes : 0, need);
   if (!aligned(workspace, 16)) return fail(QDG_ERR_MISALIGNED, "workspace must be 16-byte aligned");
   a.X = (const uint16_t*)X;
   a.A = (const uint16_t*)A;
   a.B = (const uint16_t*)B;
+  a.X_last = a.X + (M - 1) * cfg->ldx + cfg->k - 8;
+  a.A_last = a.A + (int64_t)cfg->num_adapters * cfg->num_slices * cfg->rank * cfg->k - 8;
+  a.B_last = a.B + (int64_t)cfg->num_adapters * cfg->n * cfg->rank - 8;
   a.ranks = ranks;
   a.scales = scales;
   a.sorted_ids = sorted_ids;
@@ -240,19 +257,7 @@ qdg_status qdg_lora(const qdg_lora_config* cfg, const void* X, const void* A, co
   a.num_padded = num_padded;
   a.Y = Y;
   a.partial = (float*)workspace;
-  a.ldx = cfg->ldx;
-  a.ldy = cfg->ldy;
   a.M = M;
-  a.n = (int)cfg->n;
-  a.k = (int)cfg->k;
-  a.num_adapters = cfg->num_adapters;
-  a.num_slices = cfg->num_slices;
-  a.rank = cfg->rank;
-  a.rank_pad = lora_rank_pad(cfg->rank);
-  for (int i = 0; i < cfg->num_slices; ++i) a.slice_end[i] = (int)cfg->slice_end[i];
-  a.block_m = block_m;
-  a.split = lora_split((int64_t)a.blocks * (block_m / 16), block_m, a.num_slices * a.rank_pad, cfg->k);
-  a.yf32 = cfg->otype == QDG_O_F32;
   const hipError_t e = launch_lora(a, (hipStream_t)stream);
   if (e == hipErrorInvalidConfiguration)
     return fail(QDG_ERR_UNSUPPORTED, "lora: the output has more tiles than one launch holds (2^32 threads)");

@@ -242,6 +242,9 @@ struct LoraArgs {
   const uint16_t* X;
   const uint16_t* A;       // [adapters][slices][rank][k]
   const uint16_t* B;       // [adapters][n][rank]
+  const uint16_t* X_last;  // the last place of each that has eight values
+  const uint16_t* A_last;
+  const uint16_t* B_last;
   const int32_t* ranks;    // NULL: rank
   const float* scales;     // NULL: 1
   const int32_t* sorted_ids;
@@ -254,14 +257,18 @@ struct LoraArgs {
   int n, k;
   int num_adapters, num_slices, rank, rank_pad;
   int slice_end[4];
-  int block_m, blocks;     // blocks: the most that M rows make
-  int split;
+  int block_m, block_shift;  // a block is 2^block_shift tiles of 16 rows
+  int blocks;              // the most that M rows make
+  int split;               // parts of K
+  int span;                // units of columns a workgroup of the second kernel takes
+  bool wide;               // that kernel is the one for many rows
   bool yf32;
+  bool fused;              // both products in one launch, without partials
 };
 // The most blocks of block_m rows that M rows of at most E adapters make.
 int64_t lora_blocks(int64_t M, int64_t E, int block_m);
-int lora_rank_pad(int rank);
-int lora_split(int64_t tiles, int block_m, int columns, int64_t k);
+// Sets what follows from the sizes: rank_pad, split, span and fused.
+void lora_choose(LoraArgs* a);
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
 
 #endif

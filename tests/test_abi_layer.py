@@ -93,7 +93,7 @@ def test_lora_refusals():
     assert _lora(M=0) == q.QDG_OK and _lora(M=0, X=None, ws=None) == q.QDG_OK
     assert _lora(M=-1) == INV and _lora(M=(1 << 20) + 1) == UNS
     assert _lora(n=0) == INV and _lora(k=0) == INV and _lora(rank=0) == INV and _lora(num_adapters=0) == INV
-    assert _lora(n=(1 << 26) + 1) == UNS and _lora(k=(1 << 26) + 1) == UNS and _lora(rank=257) == UNS
+    assert _lora(n=(1 << 20) + 1) == UNS and _lora(k=(1 << 20) + 1) == UNS and _lora(rank=257) == UNS
     assert _lora(num_adapters=1025) == UNS
     assert _lora(slice_ends=[]) == INV and _lora(slice_ends=[10, 20, 30, 40, 64]) == UNS
     for ends in ([32], [32, 32, 64], [40, 30, 64], [0, 64], [-1, 64], [32, 65]):
@@ -105,11 +105,12 @@ def test_lora_refusals():
         assert _lora(**{name: P + 1}) == MIS, name
     assert _lora(ranks=P + 2) == MIS and _lora(scales=P + 2) == MIS
     assert _lora(otype=q.QDG_O_F32, Y=P + 2) == MIS
-    assert _lora(ws=None) == WS and _lora(ws=P + 8) == MIS
-    need = q.qdg_lora_workspace(q.lora(64, 32, 8), 4, 16)
-    assert need > 0 and _lora(ws_bytes=need - 1) == WS
-    # 2^20 rows in tiles of 16 and 2^26 columns in units of 64: more workgroups than a launch holds
-    assert _lora(M=1 << 20, n=1 << 26) == UNS
+    assert _lora(ws=P + 8) == MIS
+    need = q.qdg_lora_workspace(q.lora(64, 16384, 8), 4, 16)
+    assert need > 0 and _lora(k=16384, ws_bytes=need - 1) == WS and _lora(k=16384, ws=None) == WS
+    assert q.qdg_lora_workspace(q.lora(64, 32, 8), 4, 16) == 0  # both products in one launch
+    # 2^20 rows in tiles of 16 and 2^20 columns in units of 64: more workgroups than a launch holds
+    assert _lora(M=1 << 20, n=1 << 20) == UNS
 
 
 def test_lora_workspace():

@@ -112,6 +112,28 @@ def test_sizes(qdg, case):
     _run(rng, pool, ids, (16, 32, 64, 128)[(case // 4) % 4], bool(case & 2), pad=(0, 1, 8)[case % 3], shift=(0, 1)[case % 2])
 
 
+@pytest.mark.parametrize("bm", [16, 32, 64, 128])
+@pytest.mark.parametrize("k", [6208, 6150, 12289])
+def test_long_k_in_two_launches(qdg, k, bm):
+    """Ranks below, at and between the tiles of 16; columns that end inside a unit of 64 or 128."""
+    for i, (rank, n) in enumerate(((1, 65), (4, 130), (8, 129), (12, 255), (16, 257), (24, 300), (32, 96), (40, 131))):
+        rng = np.random.default_rng(k + rank)
+        ids = rng.integers(-1, 3, 75).astype(np.int32)
+        pool = Pool(rng, n, k, rank, 3, ends=[n] if i & 1 else [n // 3, n], mixed=bool(i & 2))
+        assert q.qdg_lora_workspace(q.lora(n, k, rank, num_adapters=3, slice_ends=pool.ends), 75, bm) > 0
+        _run(rng, pool, ids, bm, bool(i & 1), pad=i % 3, shift=i % 2)
+
+
+def test_many_tiles_of_a_short_k(qdg):
+    """More workgroups than run at once: two launches for sizes that take one where rows are few."""
+    rng = np.random.default_rng(77)
+    for bm, M, n, rank in ((16, 1500, 4200, 8), (64, 3000, 6600, 16), (128, 2600, 8200, 32)):
+        ids = rng.integers(-1, 6, M).astype(np.int32)
+        pool = Pool(rng, n, 200, rank, 6, ends=[n // 2 + 3, n])
+        assert q.qdg_lora_workspace(q.lora(n, 200, rank, num_adapters=6, slice_ends=pool.ends), M, bm) > 0
+        _run(rng, pool, ids, bm, rank == 16)
+
+
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("ends", [[1, 2, 3, 4], [64, 100], [30, 31, 200], [512, 576, 640], [1, 300, 301, 365]])
 def test_slices(qdg, ends, f32):
