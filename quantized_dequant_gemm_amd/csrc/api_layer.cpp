@@ -176,7 +176,9 @@ qdg_status qdg_norm(const qdg_norm_config* cfg, const void* x, const void* resid
   a.layer = c.kind == QDG_NORM_LAYER;
   a.post_norm = c.post_norm != 0;
   a.wf32 = c.wtype == QDG_O_F32;
+  a.short_join = !a.post_norm && (!gate || (c.xtype == QDG_O_BF16 && !a.wf32));
   a.eps = c.eps;
+  a.inv_n = 1.0 / (double)c.n;
   a.residual_scale = c.residual_scale;
   a.weight_offset = c.weight_offset;
   a.out = o;

@@ -225,7 +225,9 @@ struct NormArgs {
   int64_t ldx, ldr, ldg, lds, M;
   int n;
   bool layer, post_norm, wf32;
+  bool short_join;          // no norm of x, and gate * x of at most 16 significant bits
   float eps, residual_scale, weight_offset;
+  double inv_n;
   RowOut out;
 };
 struct GatedArgs {

@@ -41,11 +41,12 @@ struct Raw8 {
   }
 };
 
-// Values i .. i + 7 of a row of n (i < n), 0 behind its end.
-template <bool F32>
+// Values i .. i + 7 of a row of n (i < n), 0 behind its end. EVEN: n is a
+// multiple of 8.
+template <bool F32, bool EVEN>
 __device__ __forceinline__ Raw8<F32> load8(const void* row, int i, int n) {
   Raw8<F32> r;
-  if (n < 8) {  // the same for all lanes: a row that is no chunk
+  if (!EVEN && n < 8) {  // the same for all lanes: a row that is no chunk
 #pragma unroll
     for (int j = 0; j < (F32 ? 8 : 4); ++j) {
       if constexpr (F32) {
@@ -57,7 +58,7 @@ __device__ __forceinline__ Raw8<F32> load8(const void* row, int i, int n) {
     }
     return r;
   }
-  const int at = min(i, n - 8), skip = i - at;  // values that a chunk before has
+  const int at = EVEN ? i : min(i, n - 8), skip = i - at;  // values that a chunk before has
   if constexpr (F32) {
     const u32x4_4_t a = *(const u32x4_4_t*)((const uint32_t*)row + at), b = *(const u32x4_4_t*)((const uint32_t*)row + at + 4);
 #pragma unroll
@@ -70,7 +71,7 @@ __device__ __forceinline__ Raw8<F32> load8(const void* row, int i, int n) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) r.d[j] = a[j];
   }
-  if (skip) {
+  if (!EVEN && skip) {
     constexpr int kPer = F32 ? 1 : 2, kD = F32 ? 8 : 4;  // values a dword, dwords
 #pragma unroll
     for (int b = 4; b >= kPer; b >>= 1)
@@ -87,11 +88,11 @@ __device__ __forceinline__ Raw8<F32> load8(const void* row, int i, int n) {
 }
 
 // The first values of r into values i .. of a row of n (i < n).
-template <bool F32>
+template <bool F32, bool EVEN>
 __device__ __forceinline__ void store8(void* row, int i, int n, Raw8<F32> r) {
   if constexpr (F32) {
     uint32_t* p = (uint32_t*)row + i;
-    if (i + 8 <= n) {
+    if (EVEN || i + 8 <= n) {
       *(u32x4_4_t*)p = u32x4_4_t{r.d[0], r.d[1], r.d[2], r.d[3]};
       *(u32x4_4_t*)(p + 4) = u32x4_4_t{r.d[4], r.d[5], r.d[6], r.d[7]};
       return;
@@ -111,7 +112,7 @@ __device__ __forceinline__ void store8(void* row, int i, int n, Raw8<F32> r) {
     if (rest & 1) *p = r.d[0];
   } else {
     uint16_t* p = (uint16_t*)row + i;
-    if (i + 8 <= n) {
+    if (EVEN || i + 8 <= n) {
       *(u32x4_2_t*)p = u32x4_2_t{r.d[0], r.d[1], r.d[2], r.d[3]};
       return;
     }
@@ -132,9 +133,10 @@ __device__ __forceinline__ void store8(void* row, int i, int n, Raw8<F32> r) {
 }
 
 // Eight codes into bytes i .. of a row of n (rows of codes start at a multiple of 16).
+template <bool EVEN>
 __device__ __forceinline__ void store_codes(uint8_t* row, int i, int n, u32x2_t v) {
   uint8_t* p = row + i;
-  if (i + 8 <= n) {
+  if (EVEN || i + 8 <= n) {
     *(u32x2_t*)p = v;
     return;
   }
@@ -153,31 +155,32 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int i, int n, u32x2_t 
   if (rest & 1) *p = (uint8_t)w;
 }
 
+// The least of three magnitudes; a NaN among them comes through.
+__device__ __forceinline__ float least3(float a, float b, float c) {
+  float r;
+  asm("v_minimum3_f32 %0, |%1|, |%2|, |%3|" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // A pair of binary32 values as bf16, round to nearest even (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
   const f32x2_t v = {lo, hi};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
 
-// Weights, biases and gates: bf16 or binary32 as the call says.
-struct Vec8 {
-  float v[8];
-};
-__device__ __forceinline__ Vec8 load_vec8(const void* p, float absent, bool f32, int i, int n) {
-  Vec8 w;
-  if (!p) {
+// Between binary64 values: their chains side by side would take the registers
+// that let another wave in.
+__device__ __forceinline__ void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }
+
+// Weights, biases and gates; where there is none, `absent` for each.
+template <bool F32, bool EVEN>
+__device__ __forceinline__ Raw8<F32> load_vec8(const void* p, float absent, int i, int n) {
+  if (p) return load8<F32, EVEN>(p, i, n);
+  const uint32_t bits = __builtin_bit_cast(uint32_t, absent), word = F32 ? bits : bits >> 16 | (bits & 0xFFFF0000u);
+  Raw8<F32> r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w.v[j] = absent;
-  } else if (f32) {
-    const Raw8<true> r = load8<true>(p, i, n);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w.v[j] = r[j];
-  } else {
-    const Raw8<false> r = load8<false>(p, i, n);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w.v[j] = r[j];
-  }
-  return w;
+  for (int j = 0; j < (F32 ? 8 : 4); ++j) r.d[j] = word;
+  return r;
 }
 
 // ------------------------------------------------------------------ reductions over the TPR threads of a row
@@ -199,14 +202,43 @@ __device__ __forceinline__ float dpp(float v) {
   return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(uint32_t, v)));
 }
 
+// Rows of 16 lanes, then halves of 32, against each other: of two copies of v
+// the swap leaves both rows (halves) in every lane.
+template <bool HALVES>
+__device__ __forceinline__ void swap_rows(uint32_t v, uint32_t& x, uint32_t& y) {
+  const auto r = HALVES ? __builtin_amdgcn_permlane32_swap(v, v, false, false) : __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  x = r[0];
+  y = r[1];
+}
+template <bool HALVES, class Op>
+__device__ __forceinline__ uint32_t across(uint32_t v, Op op) {
+  uint32_t x, y;
+  swap_rows<HALVES>(v, x, y);
+  return op(x, y);
+}
+template <bool HALVES, class Op>
+__device__ __forceinline__ float across(float v, Op op) {
+  uint32_t x, y;
+  swap_rows<HALVES>(__builtin_bit_cast(uint32_t, v), x, y);
+  return op(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+template <bool HALVES, class Op>
+__device__ __forceinline__ double across(double v, Op op) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  uint32_t x0, y0, x1, y1;
+  swap_rows<HALVES>((uint32_t)u, x0, y0);
+  swap_rows<HALVES>((uint32_t)(u >> 32), x1, y1);
+  return op(__builtin_bit_cast(double, (uint64_t)x1 << 32 | x0), __builtin_bit_cast(double, (uint64_t)y1 << 32 | y0));
+}
+
 template <class T, class Op>
 __device__ __forceinline__ T wave_reduce(T v, Op op) {
   v = op(v, dpp<kXor1>(v));
   v = op(v, dpp<kXor2>(v));
   v = op(v, dpp<kMirror8>(v));
   v = op(v, dpp<kMirror16>(v));
-  v = op(v, __shfl_xor(v, 16));
-  return op(v, __shfl_xor(v, 32));
+  v = across<false>(v, op);
+  return across<true>(v, op);
 }
 
 // Two sets of one value for each wave, used in turn: whoever writes a set has
@@ -220,13 +252,16 @@ template <int TPR, class T, class Op>
 __device__ __forceinline__ T row_reduce(T v, Op op, Buffers& b, int& turn) {
   v = wave_reduce(v, op);
   if constexpr (TPR > 64) {
+    constexpr int kWaves = TPR / 64;  // 4, 8 or 16: a lane reads one, DPP joins them
     T* set = (T*)b.v[turn];
     turn ^= 1;
     if ((threadIdx.x & 63) == 0) set[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = set[0];
-#pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) v = op(v, set[w]);
+    v = set[threadIdx.x & (kWaves - 1)];
+    v = op(v, dpp<kXor1>(v));
+    v = op(v, dpp<kXor2>(v));
+    if constexpr (kWaves > 4) v = op(v, dpp<kMirror8>(v));
+    if constexpr (kWaves > 8) v = op(v, dpp<kMirror16>(v));
   }
   return v;
 }
@@ -278,16 +313,30 @@ __device__ __forceinline__ u32x2_t encode_int8x8_finite(const Raw8<false>& o, fl
   return out;
 }
 
-// The bf16 values o of a row (chunk c of thread t: values 8 (c TPR + t) and on;
-// 0 behind the end) as rows and codes.
-template <int TPR, int CH>
+// The codes of the fp8 rule for a finite group: no product is above
+// 448 (1 + 2^-23), which rounds to 448 (the next code would begin at 464).
+__device__ __forceinline__ u32x2_t encode_fp8x8_finite(const float (&f)[8], float inv) {
+  u32x2_t out;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * j] * inv, f[4 * j + 1] * inv, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * j + 2] * inv, f[4 * j + 3] * inv, w, true);
+    out[j] = (uint32_t)w;
+  }
+  return out;
+}
+
+// The bf16 values o of a row (chunk c of thread t: values 8 (c TPR + t) and on,
+// with t counted from the row's or its piece's start; 0 behind the end) as rows
+// and codes. int8 codes need the whole row, groups and blocks only theirs.
+template <int TPR, int CH, bool EVEN>
 __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, int64_t row, int t, const RowOut& out,
                                            Buffers& buf, int& turn) {
   if (out.rows) {
     uint16_t* p = out.rows + row * out.ld;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if ((c * TPR + t) * 8 < n) store8<false>(p, (c * TPR + t) * 8, n, o[c]);
+      if ((c * TPR + t) * 8 < n) store8<false, EVEN>(p, (c * TPR + t) * 8, n, o[c]);
   }
   if (out.quant == QDG_Q_NONE) return;
   uint8_t* q = out.qa + row * out.ldq;
@@ -322,7 +371,7 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
       if ((c * TPR + t) * 8 < n) {
         uint32_t code[2];
         encode_zp<4>(o[c].d, z, code);
-        store_codes(q, (c * TPR + t) * 8, n, u32x2_t{code[0], code[1]});
+        store_codes<EVEN>(q, (c * TPR + t) * 8, n, u32x2_t{code[0], code[1]});
       }
     return;
   }
@@ -355,7 +404,7 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
           for (int j = 0; j < 8; ++j) f[j] = o[c][j];
           code = encode_int8x8(f, inv);
         }
-        store_codes(q, (c * TPR + t) * 8, n, code);
+        store_codes<EVEN>(q, (c * TPR + t) * 8, n, code);
       }
     return;
   }
@@ -373,7 +422,8 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
     }
     word = halves_max(word);
     float m = bf16_to_f32(word);
-    if (__any(word > 0x7F80u)) {  // a NaN does not count
+    const bool finite = !__any(word >= 0x7F80u);
+    if (!finite) {  // a NaN does not count
       m = amax8(o[c]);
       m = fmaxf(m, dpp<kXor1>(m));
       m = fmaxf(m, dpp<kXor2>(m));
@@ -389,7 +439,8 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
     for (int j = 0; j < 8; ++j) f[j] = o[c][j];
     const bool nz = m > 0.f;
     if (fp8) {
-      *(u32x2_t*)(q + i) = nz ? encode_fp8x8(f, __fdiv_rn(448.0f, m)) : u32x2_t{0, 0};
+      const float inv = nz ? __fdiv_rn(448.0f, m) : 0.f;
+      *(u32x2_t*)(q + i) = !nz ? u32x2_t{0, 0} : finite && inv < 0x1p120f ? encode_fp8x8_finite(f, inv) : encode_fp8x8(f, inv);
       if ((t & 15) == 0) ((float*)out.scales)[row * (n / 128) + i / 128] = nz ? __fdiv_rn(m, 448.0f) : 1.0f;
     } else {
       const uint32_t e8 = nz ? fp4_block_exponent(m) : 0u;
@@ -400,10 +451,6 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
 }
 
 // ------------------------------------------------------------------ doubt
-// Between binary64 values: their chains side by side would take the registers
-// that let another wave in.
-__device__ __forceinline__ void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }
-
 // y is a binary32 value with an error of at most ULPS units in its last place:
 // near enough to the middle of two bf16 numbers (low half 0x8000) it leaves the
 // rounding open. 0 to 2 ULPS (in the high half) there, more elsewhere.
@@ -415,71 +462,104 @@ template <int ULPS>
 constexpr uint32_t kMiddle = (uint32_t)(2 * ULPS) << 16 | 0xFFFFu;
 
 // ------------------------------------------------------------------ norms
-// 1 / sqrt(mean of squares + eps) of the row v, and with LAYER its mean.
+// kPlain: an RMS norm of the stream with bf16 weights, no bias, a join that one
+// rounding of binary32 settles, and rows of whole chunks. kEven: anything with
+// bf16 weights in rows of whole chunks.
+enum { kPlain, kEven, kGeneral, kF32Weights };
+
+// 1 / sqrt(x): v_rsq_f64 (2^-14 or better) and three steps of Newton's
+// iteration, each of which squares the error; 0 and infinity stay as they are.
+__device__ __forceinline__ double inverse_root(double x) {
+  double y = __builtin_amdgcn_rsq(x);
+  if (!(x > 0.0) || !(x < __builtin_inf())) return y;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const double e = __builtin_fma(-x * y, y, 1.0);  // 1 - x y^2
+    y = __builtin_fma(0.5 * y, e, y);
+  }
+  return y;
+}
+
+// 1 / sqrt(mean of squares + eps) of the row v, and with LAYER its mean. The
+// variance is the mean of squares less the mean's square, which keeps 46 bits
+// unless the mean is more than four deviations off 0; a row that lies further
+// off is summed again around its mean.
 template <int TPR, int CH, bool F32>
-__device__ __forceinline__ void row_stats(Raw8<F32> (&v)[CH], int n, int t, bool layer, float eps, double& mean,
+__device__ __forceinline__ void row_stats(Raw8<F32> (&v)[CH], int n, int t, bool layer, float eps, double inv_n, double& mean,
                                           double& rs, Buffers& buf, int& turn) {
   mean = 0.0;
-  double s = 0.0;
-  if (layer) {
+  double s = 0.0, sq = 0.0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += (double)v[c][j];
-      v[c].renew();
-    }
-    mean = row_sum<TPR>(s, buf, turn) / (double)n;
-    s = 0.0;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int rest = n - (c * TPR + t) * 8;  // the zeros behind the end do not count
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double d = j < rest ? (double)v[c][j] - mean : 0.0;
-        s = __builtin_fma(d, d, s);
-        one_at_a_time();
-      }
-      v[c].renew();
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
+  for (int c = 0; c < CH; ++c) {
+    if (layer) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const double d = (double)v[c][j];
-        s = __builtin_fma(d, d, s);
+        s += d;
+        sq = __builtin_fma(d, d, sq);
       }
-      v[c].renew();
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double d = (double)v[c][j];
+        sq = __builtin_fma(d, d, sq);
+      }
+    }
+    v[c].renew();
+  }
+  if (layer) mean = row_sum<TPR>(s, buf, turn) * inv_n;
+  double var = row_sum<TPR>(sq, buf, turn) * inv_n;
+  if (layer) {
+    var -= mean * mean;
+    if (!(var * 16.0 > mean * mean)) {  // the same for all threads of the row
+      sq = 0.0;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int rest = n - (c * TPR + t) * 8;  // the zeros behind the end do not count
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const double d = j < rest ? (double)v[c][j] - mean : 0.0;
+          sq = __builtin_fma(d, d, sq);
+          one_at_a_time();
+        }
+        v[c].renew();
+      }
+      var = row_sum<TPR>(sq, buf, turn) * inv_n;
     }
   }
-  rs = 1.0 / sqrt(row_sum<TPR>(s, buf, turn) / (double)n + (double)eps);
+  rs = inverse_root(var + (double)eps);
 }
 
 // What is absent is neutral: a factor 1, a term -0 (which leaves a sum its sign).
-// The new stream of eight values: residual_scale * r + gate * t. PLAIN: the
-// product has at most 16 significant bits, the sum one rounding.
-template <bool PLAIN, bool XF, bool RF>
-__device__ __forceinline__ Raw8<RF> join8(const NormArgs& a, const Raw8<XF>& x, const Raw8<RF>& r, const void* gate, int i,
+// The new stream of eight values: residual_scale * r + gate * t. Without a norm
+// of x and with a product of at most 16 significant bits (short), that is one
+// rounding of binary32.
+template <bool PLAIN, bool XF, bool RF, bool WF, bool EVEN>
+__device__ __forceinline__ Raw8<RF> join8(const NormArgs& a, const Raw8<XF>& x, const Raw8<RF>& r, const Raw8<WF>& g, int i,
                                           double mean, double rs) {
   const int n = a.n;
   const float scale = a.residual ? a.residual_scale : -1.0f;  // of zeros
   float v[8];
-  const Vec8 g = load_vec8(gate, 1.0f, !PLAIN && a.wf32, i, n);
-  if constexpr (PLAIN) {
+  if (PLAIN || a.short_join) {
+    if (a.gate) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(scale, r[j], x[j] * g.v[j]);
+      for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(scale, r[j], x[j] * g[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(scale, r[j], x[j]);
+    }
   } else {
-    const Vec8 w = load_vec8(a.post_weight, 1.0f, a.wf32, i, n), b = load_vec8(a.post_bias, -0.0f, a.wf32, i, n);
+    const Raw8<WF> w = load_vec8<WF, EVEN>(a.post_weight, 1.0f, i, n), b = load_vec8<WF, EVEN>(a.post_bias, -0.0f, i, n);
     const double offset = a.post_weight ? (double)a.weight_offset : 0.0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      double d = ((double)x[j] - mean) * rs * ((double)w.v[j] + offset) + (double)b.v[j];
-      d = __builtin_fma((double)scale, (double)r[j], d * (double)g.v[j]);
+      double d = ((double)x[j] - mean) * rs * ((double)w[j] + offset) + (double)b[j];
+      d = __builtin_fma((double)scale, (double)r[j], d * (double)g[j]);
       v[j] = (float)d;
-      one_at_a_time();
+      if (j & 1) one_at_a_time();
     }
     const int rest = n - i;
-    if (rest < 8) {
+    if (!EVEN && rest < 8) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = j < rest ? v[j] : 0.f;
     }
@@ -495,62 +575,61 @@ __device__ __forceinline__ Raw8<RF> join8(const NormArgs& a, const Raw8<XF>& x, 
   return s;
 }
 
-// Eight normed values. q = rs * w and y = s * q carry four roundings of 2^-24
-// (rs, w + offset, both products): 4 units in the last place of y, 6 are
-// allowed for. Not PLAIN (a bias or a mean): y = m + b, with m's error, the
-// rounding of s - mean and its own one within 2^-21 |m| + 2^-23 |b|; the
-// roundings of both ends of that interval are compared. Rows and weights whose
-// products leave the middle of binary32's range are computed in binary64.
-template <bool PLAIN, bool RF>
-__device__ __forceinline__ Raw8<false> norm8(const NormArgs& a, const Raw8<RF>& s, const Vec8& w, const Vec8& b, int i,
+// Eight normed values. y = (s rs) w carries four roundings of 2^-24 (rs,
+// w + offset, both products): 4 units in the last place of y, 6 are allowed for.
+// Not PLAIN (a bias or a mean): m = ((s - mean) rs) w, the mean in two binary32
+// parts, y = m + b; m's error, with two more roundings, and the sum's are within
+// 2^-21 |m| + 2^-23 |b| + 2^-44 |mean rs w|, and the roundings of both ends of
+// that interval are compared. Where (s - mean) rs or y is below 2^-100, or rs
+// leaves the middle of binary32's range, binary64 decides.
+template <bool PLAIN, bool RF, bool WF, bool EVEN>
+__device__ __forceinline__ Raw8<false> norm8(const NormArgs& a, const Raw8<RF>& s, const Raw8<WF>& w, const Raw8<WF>& b, int i,
                                              double mean, double rs, bool in_range) {
   Raw8<false> o;
   const float rs32 = (float)rs, offset = a.weight ? a.weight_offset : 0.f;
+  float least = __builtin_inff();
   bool doubt = !in_range;
-  float q[8], q_most = 0.f, q_least = __builtin_inff();
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    q[j] = rs32 * (w.v[j] + offset);
-    q_most = fmaxf(q_most, fabsf(q[j]));
-    q_least = fminf(q_least, fabsf(q[j]));
-  }
-  doubt |= !(q_least > 0x1p-100f) || !(q_most < 0x1p100f);
   if constexpr (PLAIN) {
     uint32_t near = ~0u;
-    float y[8], least = __builtin_inff();
+    float y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      y[j] = s[j] * q[j];
+      const float p = s[j] * rs32;
+      y[j] = p * (w[j] + offset);
       near = min(near, to_middle<6>(y[j]));
-      least = fminf(least, fabsf(y[j]));
+      least = least3(least, p, y[j]);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) o.d[j] = to_bf16_pair(y[2 * j], y[2 * j + 1]);
-    doubt |= near <= kMiddle<6> || !(least > 0x1p-100f);
+    doubt |= near <= kMiddle<6>;
   } else {
     uint32_t differ = 0;
+    const float mean_hi = (float)mean, mean_lo = (float)(mean - (double)mean_hi), off = fabsf(mean_hi) * rs32 * 0x1p-44f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float lo[2], hi[2];
+      float lo[2], hi[2], p[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float m = (float)((double)s[2 * j + h] - mean) * q[2 * j + h], bj = b.v[2 * j + h], sum = m + bj;
-        const float e = __builtin_fmaf(fabsf(m), 0x1p-21f, __builtin_fmaf(fabsf(bj), 0x1p-23f, 0x1p-110f));
+        const float wj = w[2 * j + h] + offset, bj = b[2 * j + h];
+        p[h] = ((s[2 * j + h] - mean_hi) - mean_lo) * rs32;
+        const float m = p[h] * wj, sum = m + bj;
+        const float e = __builtin_fmaf(fabsf(m), 0x1p-21f, __builtin_fmaf(fabsf(bj), 0x1p-23f, __builtin_fmaf(off, fabsf(wj), 0x1p-110f)));
         lo[h] = sum - e;
         hi[h] = sum + e;
       }
+      least = least3(least, p[0], p[1]);
       o.d[j] = to_bf16_pair(lo[0], lo[1]);
       differ |= o.d[j] ^ to_bf16_pair(hi[0], hi[1]);
-      one_at_a_time();
     }
     doubt |= differ != 0;
   }
+  doubt |= !(least > 0x1p-100f);
   if (doubt) {
     float z[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      double d = (PLAIN ? (double)s[j] : (double)s[j] - mean) * rs * ((double)w.v[j] + (double)offset);
-      if (!PLAIN) d += (double)b.v[j];
+      double d = (PLAIN ? (double)s[j] : (double)s[j] - mean) * rs * ((double)w[j] + (double)offset);
+      if (!PLAIN) d += (double)b[j];
       z[j] = (float)d;
       one_at_a_time();
     }
@@ -558,15 +637,16 @@ __device__ __forceinline__ Raw8<false> norm8(const NormArgs& a, const Raw8<RF>& 
     for (int j = 0; j < 4; ++j) o.d[j] = to_bf16_pair(z[2 * j], z[2 * j + 1]);
   }
   const int rest = a.n - i;
-  if (rest < 8) {
+  if (!EVEN && rest < 8) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) o.d[j] &= 2 * j + 1 < rest ? ~0u : 2 * j < rest ? 0xFFFFu : 0u;
   }
   return o;
 }
 
-template <int TPR, int CH, bool XF, bool RF, bool PLAIN>
+template <int TPR, int CH, bool XF, bool RF, int MODE>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
+  constexpr bool PLAIN = MODE == kPlain, WF = MODE == kF32Weights, EVEN = MODE == kPlain || MODE == kEven;
   __shared__ Buffers buf;
   int turn = 0;
   constexpr int kThreads = TPR < 256 ? 256 : TPR, RPB = kThreads / TPR;
@@ -576,32 +656,35 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
     if (TPR < 256 && row >= a.M) break;  // whole waves: no barrier below
     const char* x = (const char*)a.x + row * a.ldx * (XF ? 4 : 2);
     const char* r = (const char*)a.residual + row * a.ldr * (RF ? 4 : 2);
-    const char* g = a.gate ? (const char*)a.gate + row * a.ldg * (a.wf32 ? 4 : 2) : nullptr;
+    const char* g = a.gate ? (const char*)a.gate + row * a.ldg * (WF ? 4 : 2) : nullptr;
     Raw8<XF> v[CH];
     Raw8<RF> s[CH];
+    Raw8<WF> gate[CH], weight[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       v[c] = {};
       s[c] = {};
       const int i = (c * TPR + t) * 8;
       if (i < n) {
-        v[c] = load8<XF>(x, i, n);
-        if (a.residual) s[c] = load8<RF>(r, i, n);
+        v[c] = load8<XF, EVEN>(x, i, n);
+        if (a.residual) s[c] = load8<RF, EVEN>(r, i, n);
+        gate[c] = load_vec8<WF, EVEN>(g, 1.0f, i, n);
+        weight[c] = load_vec8<WF, EVEN>(a.weight, 1.0f, i, n);
       }
     }
     double mean = 0.0, rs = 1.0;
-    if (!PLAIN && a.post_norm) row_stats<TPR, CH, XF>(v, n, t, a.layer, a.eps, mean, rs, buf, turn);
+    if (!PLAIN && a.post_norm) row_stats<TPR, CH, XF>(v, n, t, a.layer, a.eps, a.inv_n, mean, rs, buf, turn);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (c * TPR + t) * 8;
       if (i < n) {
-        s[c] = join8<PLAIN, XF, RF>(a, v[c], s[c], g, i, mean, rs);
-        if (a.residual_out) store8<RF>((char*)a.residual_out + row * a.lds * (RF ? 4 : 2), i, n, s[c]);
+        s[c] = join8<PLAIN, XF, RF, WF, EVEN>(a, v[c], s[c], gate[c], i, mean, rs);
+        if (a.residual_out) store8<RF, EVEN>((char*)a.residual_out + row * a.lds * (RF ? 4 : 2), i, n, s[c]);
       }
       s[c].renew();
     }
     if (!a.out.rows && a.out.quant == QDG_Q_NONE) continue;
-    row_stats<TPR, CH, RF>(s, n, t, !PLAIN && a.layer, a.eps, mean, rs, buf, turn);
+    row_stats<TPR, CH, RF>(s, n, t, !PLAIN && a.layer, a.eps, a.inv_n, mean, rs, buf, turn);
     const bool in_range = rs > 0x1p-60 && rs < 0x1p60;
     Raw8<false> o[CH];
 #pragma unroll
@@ -609,13 +692,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
       const int i = (c * TPR + t) * 8;
       o[c] = {};
       if (i < n) {
-        const Vec8 w = load_vec8(a.weight, 1.0f, !PLAIN && a.wf32, i, n);
-        const Vec8 b = load_vec8(PLAIN ? nullptr : a.bias, -0.0f, a.wf32, i, n);
-        o[c] = norm8<PLAIN, RF>(a, s[c], w, b, i, mean, rs, in_range);
+        const Raw8<WF> b = load_vec8<WF, EVEN>(PLAIN ? nullptr : a.bias, -0.0f, i, n);
+        o[c] = norm8<PLAIN, RF, WF, EVEN>(a, s[c], weight[c], b, i, mean, rs, in_range);
       }
       o[c].renew();
     }
-    finish_row<TPR, CH>(o, n, row, t, a.out, buf, turn);
+    finish_row<TPR, CH, EVEN>(o, n, row, t, a.out, buf, turn);
   }
 }
 
@@ -635,59 +717,93 @@ __device__ __forceinline__ double act64(double g, int act) {
 // the last place, 11 are allowed for. GELU's t = -g (c1 + c3 g^2) is itself off
 // by up to 2.5 roundings and those of its constants, 4 2^-24 |t|, which the
 // exponential turns into as much times ln 2 of its value: within 2^-24 (22 + 4 |t|)
-// all told, and both ends of that interval are compared. Values below 2^-100 are
-// computed in binary64.
+// all told, and both ends of that interval are compared. Where the value or the
+// reciprocal is below 2^-100 (or a NaN), binary64 decides: above, u times the
+// reciprocal keeps its digits (a product below binary32's normal range needs a
+// gate above 2^26, whose reciprocal is 1, to come back above 2^-100).
 template <bool YF>
 __device__ __forceinline__ Raw8<false> gated8(const Raw8<YF>& g, const Raw8<YF>& u, int act) {
   Raw8<false> o;
-  float y[8];
-  uint32_t open = 0;  // values whose bf16 number is open
+  float y[8], off[8], least = __builtin_inff();
+  bool doubt;
   if (act == QDG_ACT_SILU) {
+    uint32_t near = ~0u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       constexpr float kL = 1.44269504f, kLo = 1.92596303e-8f, kLn2 = 0.69314718f;  // log2(e) = kL + kLo
-      const float h = __builtin_amdgcn_fmed3f(g[j], -128.f, 128.f);
+      const float h = __builtin_amdgcn_fmed3f(g[j], -256.f, 256.f);
       const float t = -h * kL, r = __builtin_fmaf(-h, kLo, __builtin_fmaf(-h, kL, -t));
-      const float p = __builtin_amdgcn_exp2f(t);
-      const float e = __builtin_fmaf(p, r * kLn2, p);
-      y[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + e) * u[j];
-      open |= to_middle<11>(y[j]) <= kMiddle<11> || !(fabsf(y[j]) > 0x1p-100f) ? 1u << j : 0u;
+      const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(r, kLn2, 1.0f);  // infinite from t = 128 on
+      const float rc = __builtin_amdgcn_rcpf(1.0f + e);
+      y[j] = (u[j] * rc) * g[j];
+      near = min(near, to_middle<11>(y[j]));
+      least = least3(least, y[j], rc);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) o.d[j] = to_bf16_pair(y[2 * j], y[2 * j + 1]);
+    doubt = near <= kMiddle<11>;
   } else {
+    uint32_t differ = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       constexpr float kC1 = -2.3022082f, kC3 = -0.10294324f;  // -2 sqrt(2 / pi) log2(e), and 0.044715 of it
       const float h = __builtin_amdgcn_fmed3f(g[j], -32.f, 32.f);
       const float t = h * __builtin_fmaf(h * h, kC3, kC1);
-      const float e = __builtin_amdgcn_exp2f(t);
-      y[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + e) * u[j];
-      const float off = __builtin_fmaf(fabsf(t), 0x1p-22f, 22 * 0x1p-24f) * y[j];
-      const uint32_t both = to_bf16_pair(y[j] - off, y[j] + off);
-      open |= (both & 0xFFFFu) != both >> 16 || !(fabsf(y[j]) > 0x1p-100f) ? 1u << j : 0u;
+      const float rc = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
+      y[j] = (u[j] * rc) * g[j];
+      off[j] = __builtin_fmaf(fabsf(t), 0x1p-22f, 22 * 0x1p-24f) * y[j];
+      least = least3(least, y[j], rc);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o.d[j] = to_bf16_pair(y[2 * j], y[2 * j + 1]);
+    for (int j = 0; j < 4; ++j) {
+      o.d[j] = to_bf16_pair(y[2 * j] - off[2 * j], y[2 * j + 1] - off[2 * j + 1]);
+      differ |= o.d[j] ^ to_bf16_pair(y[2 * j] + off[2 * j], y[2 * j + 1] + off[2 * j + 1]);
+    }
+    doubt = differ != 0;
   }
-  if (open) {
+  if (doubt || !(least > 0x1p-100f)) {  // which values' numbers are open? A lane's are computed one after the other.
+    uint32_t open = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (open >> j & 1) {
-        const uint32_t b = to_bf16_pair((float)(act64((double)g[j], act) * (double)u[j]), 0.f);
-        o.d[j >> 1] = j & 1 ? (o.d[j >> 1] & 0xFFFFu) | b << 16 : (o.d[j >> 1] & 0xFFFF0000u) | (b & 0xFFFFu);
-        one_at_a_time();
+    for (int j = 0; j < 4; ++j) o.d[j] = to_bf16_pair(y[2 * j], y[2 * j + 1]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // the reciprocal is above 2^-100 with these gates
+      bool is = !(fabsf(y[j]) > 0x1p-100f) || !(g[j] > (act == QDG_ACT_SILU ? -69.f : -8.5f));
+      if (act == QDG_ACT_SILU) {
+        is |= to_middle<11>(y[j]) <= kMiddle<11>;
+      } else {
+        const uint32_t both = to_bf16_pair(y[j] - off[j], y[j] + off[j]);
+        is |= (both & 0xFFFFu) != both >> 16;
       }
+      if (y[j] == 0.f && (g[j] == 0.f || u[j] == 0.f)) is = false;  // exactly 0
+      open |= is ? 1u << j : 0u;
+    }
+    while (open) {
+      const uint32_t bit = open & -open;
+      open ^= bit;
+      float gj = 0.f, uj = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        gj = bit >> j & 1 ? g[j] : gj;
+        uj = bit >> j & 1 ? u[j] : uj;
+      }
+      const uint32_t b = to_bf16_pair((float)(act64((double)gj, act) * (double)uj), 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (bit >> j & 1) o.d[j >> 1] = j & 1 ? (o.d[j >> 1] & 0xFFFFu) | b << 16 : (o.d[j >> 1] & 0xFFFF0000u) | (b & 0xFFFFu);
+    }
   }
   return o;
 }
 
-template <int TPR, int CH, bool YF>
+// A piece of TPR * CH * 8 columns of a row for each blockIdx.y: one for int8
+// codes, which need the row's largest value.
+template <int TPR, int CH, bool YF, bool EVEN>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_kernel(GatedArgs a) {
   __shared__ Buffers buf;
   int turn = 0;
   constexpr int kThreads = TPR < 256 ? 256 : TPR, RPB = kThreads / TPR;
-  const int t = threadIdx.x % TPR, n = a.n;
+  const int t = threadIdx.x % TPR + blockIdx.y * (TPR * CH), n = a.n;
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.M; r0 += (int64_t)gridDim.x * RPB) {
     const int64_t row = r0 + threadIdx.x / TPR;
     if (TPR < 256 && row >= a.M) break;  // whole waves: no barrier below
@@ -698,8 +814,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_kernel(GatedArgs 
       const int i = (c * TPR + t) * 8;
       g[c] = u[c] = {};
       if (i < n) {
-        g[c] = load8<YF>(y, i, n);
-        u[c] = load8<YF>(y + (int64_t)n * (YF ? 4 : 2), i, n);
+        g[c] = load8<YF, EVEN>(y, i, n);
+        u[c] = load8<YF, EVEN>(y + (int64_t)n * (YF ? 4 : 2), i, n);
       }
     }
     Raw8<false> o[CH];
@@ -709,7 +825,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_kernel(GatedArgs 
       if ((c * TPR + t) * 8 < n) o[c] = gated8<YF>(g[c], u[c], a.act);
       o[c].renew();
     }
-    finish_row<TPR, CH>(o, n, row, t, a.out, buf, turn);
+    finish_row<TPR, CH, EVEN>(o, n, row, t, a.out, buf, turn);
   }
 }
 
@@ -717,40 +833,42 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_kernel(GatedArgs 
 constexpr int64_t kMaxBlocks = (int64_t)1 << 20;
 
 template <class K, class A>
-hipError_t go(K kernel, int threads, int rows_per_block, const A& a, hipStream_t s) {
-  const int64_t blocks = (a.M + rows_per_block - 1) / rows_per_block;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(threads), 0, s, a);
+hipError_t go(K kernel, int threads, int rows_per_block, const A& a, hipStream_t s, int pieces = 1) {
+  const int64_t blocks = (a.M + rows_per_block - 1) / rows_per_block, most = kMaxBlocks / pieces;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < most ? blocks : most), (unsigned)pieces), dim3(threads), 0, s, a);
   return hipGetLastError();
 }
 
-// PLAIN: an RMS norm of the stream with bf16 weights, no bias, and a join that
-// one rounding of binary32 settles; the rest keeps its registers.
-template <bool XF, bool RF, bool PLAIN>
+template <bool XF, bool RF, int MODE>
 hipError_t norm_shape(const NormArgs& a, hipStream_t s) {
-  constexpr int kCh = PLAIN ? 2 : 1;  // up to 8192 values
-  if (a.n <= 512) return go(norm_kernel<64, 1, XF, RF, PLAIN>, 256, 4, a, s);
-  if (a.n <= 2048) return go(norm_kernel<256, 1, XF, RF, PLAIN>, 256, 1, a, s);
-  if (a.n <= 4096) return go(norm_kernel<512 / kCh, kCh, XF, RF, PLAIN>, 512 / kCh, 1, a, s);
-  if (a.n <= 8192) return go(norm_kernel<1024 / kCh, kCh, XF, RF, PLAIN>, 1024 / kCh, 1, a, s);
-  if (a.n <= 16384) return go(norm_kernel<1024, 2, XF, RF, PLAIN>, 1024, 1, a, s);
-  return go(norm_kernel<1024, 4, XF, RF, PLAIN>, 1024, 1, a, s);
+  constexpr int kCh = MODE == kPlain ? 2 : 1;  // up to 8192 values
+  if (a.n <= 512) return go(norm_kernel<64, 1, XF, RF, MODE>, 256, 4, a, s);
+  if (a.n <= 2048) return go(norm_kernel<256, 1, XF, RF, MODE>, 256, 1, a, s);
+  if (a.n <= 4096) return go(norm_kernel<512 / kCh, kCh, XF, RF, MODE>, 512 / kCh, 1, a, s);
+  if (a.n <= 8192) return go(norm_kernel<1024 / kCh, kCh, XF, RF, MODE>, 1024 / kCh, 1, a, s);
+  if (a.n <= 16384) return go(norm_kernel<1024, 2, XF, RF, MODE>, 1024, 1, a, s);
+  return go(norm_kernel<1024, 4, XF, RF, MODE>, 1024, 1, a, s);
 }
 
 template <bool XF, bool RF>
 hipError_t norm_kind(const NormArgs& a, hipStream_t s) {
-  const bool plain = !a.post_norm && !a.layer && !a.bias && !a.wf32 && !(XF && a.gate);
-  return plain ? norm_shape<XF, RF, true>(a, s) : norm_shape<XF, RF, false>(a, s);
+  if (a.wf32) return norm_shape<XF, RF, kF32Weights>(a, s);
+  if (a.n % 8) return norm_shape<XF, RF, kGeneral>(a, s);
+  const bool plain = !a.layer && !a.bias && a.short_join;
+  return plain ? norm_shape<XF, RF, kPlain>(a, s) : norm_shape<XF, RF, kEven>(a, s);
 }
 
-template <bool YF>
+template <bool YF, bool EVEN>
 hipError_t gated_shape(const GatedArgs& a, hipStream_t s) {
-  if (a.n <= 512) return go(gated_kernel<64, 1, YF>, 256, 4, a, s);
-  if (a.n <= 2048) return go(gated_kernel<256, 1, YF>, 256, 1, a, s);
-  if (a.n <= 4096) return go(gated_kernel<256, 2, YF>, 256, 1, a, s);
-  if (a.n <= 8192) return go(gated_kernel<512, 2, YF>, 512, 1, a, s);
-  if (a.n <= 16384) return go(gated_kernel<1024, 2, YF>, 1024, 1, a, s);
-  if (a.n <= 32768) return go(gated_kernel<1024, 4, YF>, 1024, 1, a, s);
-  return go(gated_kernel<1024, 8, YF>, 1024, 1, a, s);
+  if (a.n <= 512) return go(gated_kernel<64, 1, YF, EVEN>, 256, 4, a, s);
+  if (a.n <= 2048) return go(gated_kernel<256, 1, YF, EVEN>, 256, 1, a, s);
+  if (a.n <= 4096) return go(gated_kernel<256, 2, YF, EVEN>, 256, 1, a, s);
+  if (a.out.quant != QDG_Q_INT8 && a.out.quant != QDG_Q_INT8_ZP)
+    return go(gated_kernel<256, 2, YF, EVEN>, 256, 1, a, s, (a.n + 4095) / 4096);
+  if (a.n <= 8192) return go(gated_kernel<512, 2, YF, EVEN>, 512, 1, a, s);
+  if (a.n <= 16384) return go(gated_kernel<1024, 2, YF, EVEN>, 1024, 1, a, s);
+  if (a.n <= 32768) return go(gated_kernel<1024, 4, YF, EVEN>, 1024, 1, a, s);
+  return go(gated_kernel<1024, 8, YF, EVEN>, 1024, 1, a, s);
 }
 
 }  // namespace
@@ -761,7 +879,8 @@ hipError_t launch_norm(const NormArgs& a, bool xf32, bool rf32, hipStream_t s) {
 }
 
 hipError_t launch_gated_act(const GatedArgs& a, bool yf32, hipStream_t s) {
-  return yf32 ? gated_shape<true>(a, s) : gated_shape<false>(a, s);
+  if (a.n % 8) return yf32 ? gated_shape<true, false>(a, s) : gated_shape<false, false>(a, s);
+  return yf32 ? gated_shape<true, true>(a, s) : gated_shape<false, true>(a, s);
 }
 
 }  // namespace qdg

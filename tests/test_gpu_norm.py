@@ -412,3 +412,41 @@ def test_replayed_graph_and_other_stream(qdg):
         np.testing.assert_array_equal(H.to_f64(stream_rows), s)
         out.check(bits)
         gated.check(layer.gated_act(codecs.bf16_bits_to_f64(bits)))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gates_and_factors_far_apart(qdg, act):
+    """Gates near 0 and far below it beside large factors: the quotient alone would leave binary32's normal range."""
+    rng = np.random.default_rng(21)
+    M, n = 8, 1024
+    g = np.concatenate([-rng.uniform(80.0, 100.0, n // 4), -rng.uniform(8.0, 11.0, n // 4),
+                        10.0 ** rng.uniform(-44, -30, n // 4), -(10.0 ** rng.uniform(-44, -30, n // 4))])
+    y = np.empty((M, 2 * n), np.float32)
+    y[:, :n] = rng.permutation(g).astype(np.float32)
+    y[:, n:] = (10.0 ** rng.uniform(0, 38, (M, n)) * rng.choice([-1, 1], (M, n))).astype(np.float32)
+    t = torch.from_numpy(y).cuda()
+    out = Out(M, n, "none", True)
+    q.qdg_gated_act(q.gated_act(n, act=q.QDG_ACT_SILU if act == "silu" else q.QDG_ACT_GELU_TANH, ytype=q.QDG_O_F32),
+                    t.data_ptr(), M, out.args()[0], stream=q.current_stream())
+    torch.cuda.synchronize()
+    out.check(layer.gated_act(y.astype(np.float64), act))
+
+
+def test_stream_and_weights_far_apart(qdg):
+    """Products of factors at the ends of binary32's range."""
+    rng = np.random.default_rng(22)
+    M, n = 6, 1024
+    r = (10.0 ** rng.uniform(-40, 0, (M, n))).astype(np.float32)
+    r[3:] = (10.0 ** rng.uniform(0, 38, (3, n))).astype(np.float32)
+    w = (10.0 ** rng.uniform(-38, 38, n) * rng.choice([-1, 1], n)).astype(np.float32)
+    b = (10.0 ** rng.uniform(-38, 38, n)).astype(np.float32)
+    dr, dw, db = (torch.from_numpy(v).cuda() for v in (r, w, b))
+    for wf32, bias in ((True, False), (True, True), (False, False)):
+        cw = dw if wf32 else dw.to(torch.bfloat16)
+        out = Out(M, n, "none", True)
+        cfg = q.norm(n, xtype=q.QDG_O_F32, rtype=q.QDG_O_F32, wtype=q.QDG_O_F32 if wf32 else q.QDG_O_BF16)
+        q.qdg_norm(cfg, dr.data_ptr(), None, None, None, None, cw.data_ptr(), db.data_ptr() if bias else None, M, None,
+                   out.args()[0], stream=q.current_stream())
+        torch.cuda.synchronize()
+        _, bits = layer.norm(r, weight=H.to_f64(cw), bias=b if bias else None, r_f32=True)
+        out.check(bits)
