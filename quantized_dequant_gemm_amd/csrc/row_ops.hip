@@ -645,7 +645,7 @@ __device__ __forceinline__ Raw8<false> norm8(const NormArgs& a, const Raw8<RF>& 
 }
 
 template <int TPR, int CH, bool XF, bool RF, int MODE>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR, MODE == kPlain && TPR < 1024 ? 5 : 4) void norm_kernel(NormArgs a) {
   constexpr bool PLAIN = MODE == kPlain, WF = MODE == kF32Weights, EVEN = MODE == kPlain || MODE == kEven;
   __shared__ Buffers buf;
   int turn = 0;
@@ -799,7 +799,7 @@ __device__ __forceinline__ Raw8<false> gated8(const Raw8<YF>& g, const Raw8<YF>&
 // A piece of TPR * CH * 8 columns of a row for each blockIdx.y: one for int8
 // codes, which need the row's largest value.
 template <int TPR, int CH, bool YF, bool EVEN>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_kernel(GatedArgs a) {
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void gated_kernel(GatedArgs a) {
   __shared__ Buffers buf;
   int turn = 0;
   constexpr int kThreads = TPR < 256 ? 256 : TPR, RPB = kThreads / TPR;
@@ -841,7 +841,7 @@ hipError_t go(K kernel, int threads, int rows_per_block, const A& a, hipStream_t
 
 template <bool XF, bool RF, int MODE>
 hipError_t norm_shape(const NormArgs& a, hipStream_t s) {
-  constexpr int kCh = MODE == kPlain ? 2 : 1;  // up to 8192 values
+  constexpr int kCh = MODE == kPlain || MODE == kEven ? 2 : 1;  // up to 8192 values
   if (a.n <= 512) return go(norm_kernel<64, 1, XF, RF, MODE>, 256, 4, a, s);
   if (a.n <= 2048) return go(norm_kernel<256, 1, XF, RF, MODE>, 256, 1, a, s);
   if (a.n <= 4096) return go(norm_kernel<512 / kCh, kCh, XF, RF, MODE>, 512 / kCh, 1, a, s);
@@ -866,7 +866,7 @@ hipError_t gated_shape(const GatedArgs& a, hipStream_t s) {
   if (a.out.quant != QDG_Q_INT8 && a.out.quant != QDG_Q_INT8_ZP)
     return go(gated_kernel<256, 2, YF, EVEN>, 256, 1, a, s, (a.n + 4095) / 4096);
   if (a.n <= 8192) return go(gated_kernel<512, 2, YF, EVEN>, 512, 1, a, s);
-  if (a.n <= 16384) return go(gated_kernel<1024, 2, YF, EVEN>, 1024, 1, a, s);
+  if (a.n <= 16384) return YF ? go(gated_kernel<1024, 2, YF, EVEN>, 1024, 1, a, s) : go(gated_kernel<512, 4, YF, EVEN>, 512, 1, a, s);
   if (a.n <= 32768) return go(gated_kernel<1024, 4, YF, EVEN>, 1024, 1, a, s);
   return go(gated_kernel<1024, 8, YF, EVEN>, 1024, 1, a, s);
 }
