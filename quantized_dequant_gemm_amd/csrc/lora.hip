@@ -504,22 +504,32 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int tiles) {
   int row[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) row[m] = row_at(a, (tile0 + m) * 16 + (lane & 15));
+  // Y and the first step's B are asked for before T is added up, and each next step's B before a product
+  OldY<MT, YF> old;
+  BTile<ODD> b;
+  int col0 = cs.j0 + wave * kUnit;
+  auto ask = [&]() {
+    b.place(a, ad, col0, cs.j1, 0);
+    b.load(a);
+    old.load(a, row, col0 + 16 * c, cs.j1 - col0 - 16 * c);
+  };
+  if (col0 < cs.j1) ask();
   terms_of<MT, YF>(a, ad, tile0, tiles, cs.slice, steps, terms);
   __syncthreads();
-  for (int unit = wave; unit < span; unit += 4) {
-    const int col0 = cs.j0 + unit * kUnit, col = col0 + 16 * c;
-    if (col0 >= cs.j1) break;
-    OldY<MT, YF> old;  // asked for first: the longest way
-    old.load(a, row, col, cs.j1 - col);
+  for (int unit = wave; unit < span && col0 < cs.j1; unit += 4) {
+    if (unit != wave) ask();
     f32x4_t acc[MT][4] = {};
     for (int s = 0; s < steps; ++s) {
-      BTile<ODD> b;
-      b.place(a, ad, col0, cs.j1, s);
-      b.load(a);
-      b.settle(a);
-      multiply_b<MT, YF>(b.v, terms, steps, s, acc);
+      BTile<ODD> now = b;
+      if (s + 1 < steps) {
+        b.place(a, ad, col0, cs.j1, s + 1);
+        b.load(a);
+      }
+      now.settle(a);
+      multiply_b<MT, YF>(now.v, terms, steps, s, acc);
     }
-    old.add_and_store(a, row, col, cs.j1 - col, acc);
+    old.add_and_store(a, row, col0 + 16 * c, cs.j1 - col0 - 16 * c, acc);
+    col0 += 4 * kUnit;
   }
 }
 
@@ -552,10 +562,13 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
   const int col0 = cs.j0 + wave * kUnit, col = col0 + 16 * c;
   const bool mine = col0 < cs.j1;
   OldY<1, YF> old;
-  BTile<ODD> b;
+  BTile<ODD> b[NT];
   if (mine) {
-    b.place(a, ad, col0, cs.j1, 0);
-    b.load(a);
+#pragma unroll
+    for (int s = 0; s < NT; ++s) {
+      b[s].place(a, ad, col0, cs.j1, s);
+      b[s].load(a);
+    }
     old.load(a, row, col, cs.j1 - col);
   }
   const int all = a.k / 64, each = (all + kFusedWaves - 1) / kFusedWaves, s0 = min(wave * each, all), s1 = min(s0 + each, all);
@@ -591,13 +604,11 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
   __syncthreads();
   if (!mine) return;
   f32x4_t acc[1][4] = {};
-  for (int s = 0; s < steps; ++s) {
-    if (s > 0) {
-      b.place(a, ad, col0, cs.j1, s);
-      b.load(a);
-    }
-    b.settle(a);
-    multiply_b<1, YF>(b.v, terms, steps, s, acc);
+#pragma unroll
+  for (int s = 0; s < NT; ++s) {
+    if (s >= steps) break;
+    b[s].settle(a);
+    multiply_b<1, YF>(b[s].v, terms, steps, s, acc);
   }
   old.add_and_store(a, row, col, cs.j1 - col, acc);
 }
@@ -613,7 +624,7 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
 // meanwhile.
 constexpr int kWide = 128, kBStep = kWide * 32 + kWide / 8 * 16;
 template <int STEPS, bool YF, bool ODD>
-__global__ __launch_bounds__(256) void lora_wide_kernel(LoraArgs a, int tiles) {
+__global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_kernel(LoraArgs a, int tiles) {
   const int span = a.span;
   __shared__ u32x4_t terms[4 * STEPS * kTerms<YF> * 64];
   __shared__ u32x4_t lds[2][STEPS * kBStep / 16];
@@ -745,7 +756,8 @@ void lora_choose(LoraArgs* a) {
   // (32) for 1024 values of k while all workgroups run at once, two launches
   // 8 to 10 us. k = 4096, n = 4096: 1 row of rank 16 6.5 against 8.6 us, 32
   // adapters of rank 32 10.1 against 9.9; k = 14336, rank 8 12.9 against 10.7.
-  a->fused = (nt + 1) * (int64_t)a->k <= 12288 && nt <= 2 && tiles * chunks_of(*a, kFusedWaves * kUnit) <= 640;
+  a->fused = (nt + 1) * (int64_t)a->k <= 12288 && nt <= 2 &&
+             tiles * chunks_of(*a, kFusedWaves * kUnit) <= (a->block_m == 16 ? 640 : 256);
   // Parts of K: 512 workgroups (two a CU) where there is that much, each wave
   // with two steps of 64 at least.
   const int mt = groups > 2 && tiles_per_group(a->block_m) > 2 ? 2 : tiles_per_group(a->block_m);
@@ -760,7 +772,7 @@ void lora_choose(LoraArgs* a) {
     const int64_t most = all / 256, by_count = all / 1024;
     a->span = clamp(t > by_count ? (t < most ? t : most) : by_count, 1, 16);
   } else {
-    a->span = clamp(tiles / (mt < 2 ? mt : 2) * chunks_of(*a, kUnit) / 2048 / 4 * 4, 4, 32);
+    a->span = clamp(tiles / (mt < 2 ? mt : 2) * chunks_of(*a, kUnit) / 768 / 4 * 4, 4, 32);
   }
 }
 
