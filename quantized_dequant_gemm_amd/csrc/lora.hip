@@ -95,6 +95,21 @@ __device__ __forceinline__ Adapter adapter_of(const LoraArgs& a, int tile0) {
   if (tile0 * 16 >= padded || e != r.id) r.rank = 0;
   return r;
 }
+// Workgroups go to the 8 XCDs in turn. In a grid that is a multiple of 8 wide
+// each XCD takes a run of the groups of `mt` tiles that hold rows, with all their
+// columns and K parts, so that an adapter's A and B come into one L2 or two, not
+// into all, and T's partials stay in theirs (one row, k = 14336, rank 16: 8.6
+// against 11.6 us with its workgroups on all XCDs). A narrower grid is that of
+// fewer than 8 groups with more workgroups each than an XCD has CUs: they are
+// spread (one row of rank 64, 28672 columns 11.7 against 18 us). -1: nothing for
+// this one.
+__device__ __forceinline__ int tile_group(const LoraArgs& a, int mt) {
+  const int groups = (scalar_load(a.num_padded) / 16 + mt - 1) / mt;
+  if (gridDim.x % 8) return (int)blockIdx.x < groups ? (int)blockIdx.x : -1;
+  const int each = (groups + 7) / 8, g = (int)(blockIdx.x % 8) * each + (int)(blockIdx.x / 8);
+  return (int)(blockIdx.x / 8) < each && g < groups ? g : -1;
+}
+
 // Row i of the grouped order, -1: padding.
 __device__ __forceinline__ int row_at(const LoraArgs& a, int i) {
   const int r = a.sorted_ids[i];
@@ -225,10 +240,12 @@ __device__ __forceinline__ void inner_sums(const LoraArgs& a, const uint16_t* co
 // workgroup = (rows, columns, K part), its four waves share the K part. What
 // padding rows read is not used.
 template <int MT, int NT, bool ODD>
-__global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int wave_steps) {
+__global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int tiles, int wave_steps) {
   __shared__ u32x4_t lds[4 * (MT + NT) * kTileBytes / 16 > 4 * MT * NT * 64 ? 4 * (MT + NT) * kTileBytes / 16 : 4 * MT * NT * 64];
   const int groups = a.num_slices * a.rank_pad / 16;
-  const int tile0 = blockIdx.x * MT, g0 = blockIdx.y * NT, part = blockIdx.z;
+  const int group = tile_group(a, MT);
+  if (group < 0 || group * MT >= tiles) return;
+  const int tile0 = group * MT, g0 = blockIdx.y * NT, part = blockIdx.z;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const uint16_t* x[MT][2];
 #pragma unroll
@@ -266,7 +283,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int wave_ste
     if (g >= groups) continue;
     const f32x4_t* v = sum + f * 64 + lane;
     const f32x4_t t = (v[0] + v[MT * NT * 64]) + (v[2 * MT * NT * 64] + v[3 * MT * NT * 64]);
-    *((f32x4_t*)a.partial + (((int64_t)part * gridDim.x * MT + tile0 + m) * groups + g) * 64 + lane) = t;
+    *((f32x4_t*)a.partial + (((int64_t)part * tiles + tile0 + m) * groups + g) * 64 + lane) = t;
   }
 }
 
@@ -496,7 +513,9 @@ template <int MT, bool YF, bool ODD>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int tiles) {
   const int span = a.span;
   extern __shared__ u32x4_t terms[];  // [MT][rank step][hi, lo and, with YF, the third][64]
-  const int tile0 = blockIdx.x * MT;
+  const int group = tile_group(a, MT);
+  if (group < 0 || group * MT >= tiles) return;
+  const int tile0 = group * MT;
   const Adapter ad = adapter_of(a, tile0);
   if (ad.rank == 0) return;
   const Columns cs = columns_of(a, blockIdx.y, span * kUnit);
@@ -504,7 +523,9 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int tiles) {
   int row[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) row[m] = row_at(a, (tile0 + m) * 16 + (lane & 15));
-  // Y and the first step's B are asked for before T is added up, and each next step's B before a product
+  // Y and the first step's B are asked for before T is added up, each next
+  // step's B before a product (more ahead costs a wave a SIMD: 250 rows of rank
+  // 64, binary32, 10 -> 16 us)
   OldY<MT, YF> old;
   BTile<ODD> b;
   int col0 = cs.j0 + wave * kUnit;
@@ -545,7 +566,7 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
   constexpr int kSumRow = NT * 64 + 1, kIn = kFusedWaves * (1 + NT) * kTileBytes / 16;
   __shared__ u32x4_t lds[kIn > kFusedWaves * kSumRow ? kIn : kFusedWaves * kSumRow];
   __shared__ u32x4_t terms[NT * kTerms<YF> * 64];
-  // a tile's workgroups are a multiple of 8 apart: on one XCD, whose L2 holds the adapter for all
+  // a tile's workgroups are on one XCD, whose L2 holds the adapter for all, while that has the CUs (grid_x)
   const int tile = blockIdx.x;
   if (tile >= tiles) return;
   const uint16_t* x[1][2];
@@ -629,7 +650,9 @@ __global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_ke
   __shared__ u32x4_t terms[4 * STEPS * kTerms<YF> * 64];
   __shared__ u32x4_t lds[2][STEPS * kBStep / 16];
   constexpr int kP = YF ? 2 : 1, kE = YF ? 4 : 8;  // pieces of a lane's row, elements a piece
-  const int tile0 = blockIdx.x * 4;
+  const int group = tile_group(a, 4);
+  if (group < 0 || group * 4 >= tiles) return;
+  const int tile0 = group * 4;
   const Adapter ad = adapter_of(a, tile0);
   if (ad.rank == 0) return;
   const Columns cs = columns_of(a, blockIdx.y, span * kWide);
@@ -778,6 +801,9 @@ void lora_choose(LoraArgs* a) {
 
 namespace {
 
+// The grid's width for groups of `each` workgroups (see tile_group).
+int64_t grid_x(int64_t groups, int64_t each) { return groups < 8 && each > 32 ? groups : (groups + 7) / 8 * 8; }
+
 // A launch holds fewer than 2^32 threads, and 65535 workgroups in y and z.
 bool too_many(int64_t x, int64_t y, int64_t z, int threads) {
   return y > 65535 || z > 65535 || x * y * z >= ((int64_t)1 << 32) / threads;
@@ -785,7 +811,7 @@ bool too_many(int64_t x, int64_t y, int64_t z, int threads) {
 
 template <bool ODD, int NT>
 hipError_t fused_nt(const LoraArgs& a, hipStream_t s) {
-  const int64_t tiles = (int64_t)a.blocks * (a.block_m / 16), x = (tiles + 7) / 8 * 8, y = chunks_of(a, kFusedWaves * kUnit);
+  const int64_t tiles = (int64_t)a.blocks * (a.block_m / 16), y = chunks_of(a, kFusedWaves * kUnit), x = grid_x(tiles, y);
   if (too_many(x, y, 1, 64 * kFusedWaves)) return hipErrorInvalidConfiguration;
   auto kernel = a.yf32 ? lora_fused_kernel<NT, true, ODD> : lora_fused_kernel<NT, false, ODD>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)x, (unsigned)y), dim3(64 * kFusedWaves), 0, s, a, (int)tiles);
@@ -795,8 +821,8 @@ hipError_t fused_nt(const LoraArgs& a, hipStream_t s) {
 template <bool ODD, int MT, int NT>
 hipError_t down(const LoraArgs& a, int64_t tiles, int64_t col_tiles, hipStream_t s) {
   const int waves = 4 * a.split;
-  hipLaunchKernelGGL((lora_down_kernel<MT, NT, ODD>), dim3((unsigned)(tiles / MT), (unsigned)col_tiles, (unsigned)a.split),
-                     dim3(256), 0, s, a, (a.k / 64 + waves - 1) / waves);
+  const dim3 grid((unsigned)grid_x(tiles / MT, col_tiles * a.split), (unsigned)col_tiles, (unsigned)a.split);
+  hipLaunchKernelGGL((lora_down_kernel<MT, NT, ODD>), grid, dim3(256), 0, s, a, (int)tiles, (a.k / 64 + waves - 1) / waves);
   return hipGetLastError();
 }
 
@@ -813,8 +839,8 @@ hipError_t two(const LoraArgs& a, hipStream_t s) {
   const int groups = a.num_slices * a.rank_pad / 16, nt = groups < 4 ? groups : 4;
   const int64_t col_tiles = (groups + nt - 1) / nt;
   constexpr int LT = MT < 2 ? MT : 2;  // row tiles where there are many columns: registers
-  const int64_t x = tiles / (a.wide ? 4 : LT), y = chunks_of(a, (int64_t)a.span * (a.wide ? kWide : kUnit));
-  if (too_many(tiles, col_tiles, a.split, 256) || too_many(x, y, 1, 256)) return hipErrorInvalidConfiguration;
+  const int64_t y = chunks_of(a, (int64_t)a.span * (a.wide ? kWide : kUnit)), x = grid_x(tiles / (a.wide ? 4 : LT), y);
+  if (too_many(tiles + 7, col_tiles, a.split, 256) || too_many(x, y, 1, 256)) return hipErrorInvalidConfiguration;
   hipError_t e;
   switch (nt) {
     case 1: e = down<ODD, MT, 1>(a, tiles, col_tiles, s); break;
