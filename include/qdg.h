@@ -771,13 +771,15 @@ typedef struct qdg_lora_config {
 } qdg_lora_config;
 
 /* Workspace bytes that serve qdg_lora for M rows and for any fewer (the inner
-   sums in binary32). The contents need no initialisation. Calls that share a
-   workspace must be ordered on one stream. */
+   sums in binary32; 0: none, both products are one launch). The contents need
+   no initialisation. Calls that share a workspace must be ordered on one
+   stream. */
 qdg_status qdg_lora_workspace(const qdg_lora_config* cfg, int64_t M, int32_t block_m, size_t* bytes);
 
-/* workspace 16-byte aligned. Errors: QDG_ERR_INVALID_ARG, QDG_ERR_MISALIGNED,
-   QDG_ERR_WORKSPACE, QDG_ERR_UNSUPPORTED (another block_m, a size past the
-   ranges above, more tiles than one launch holds). */
+/* Y must not overlap the other operands. workspace 16-byte aligned, NULL where
+   none is needed. One or two launches. Errors: QDG_ERR_INVALID_ARG,
+   QDG_ERR_MISALIGNED, QDG_ERR_WORKSPACE, QDG_ERR_UNSUPPORTED (another block_m, a
+   size past the ranges above, more tiles than one launch holds). */
 qdg_status qdg_lora(const qdg_lora_config* cfg, const void* X, const void* A, const void* B, const int32_t* ranks,
                     const float* scales, const int32_t* sorted_ids, const int32_t* block_adapter,
                     const int32_t* num_padded, int64_t M, int32_t block_m, void* Y, void* workspace, size_t ws_bytes,

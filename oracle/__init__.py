@@ -31,6 +31,8 @@ Modules
 ``codecs``  exact decoders (code -> real) and RNE encoders for each storage type
 ``quant``   producers of the standard format (weights) and activation quantizers
 ``ref``     dequantize-then-matmul references, MoE routing and the expert sort
+``ops``     routing, asymmetric int8 activations, int8 products over stored operands
+``layer``   norms with gate and residual, gated activations, low-rank adapters
 ``metrics`` comparison helpers
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``

@@ -775,11 +775,15 @@ void lora_choose(LoraArgs* a) {
   a->rank_pad = (a->rank + 15) / 16 * 16;
   const int nt = a->rank_pad / 16, groups = a->num_slices * nt;
   // One launch where T, anew for every 512 columns, costs less than the second
-  // launch and the partials: that takes 4 us and 0.6 us (16 ranks) or 0.85 us
-  // (32) for 1024 values of k while all workgroups run at once, two launches
-  // 8 to 10 us. k = 4096, n = 4096: 1 row of rank 16 6.5 against 8.6 us, 32
-  // adapters of rank 32 10.1 against 9.9; k = 14336, rank 8 12.9 against 10.7.
-  a->fused = (nt + 1) * (int64_t)a->k <= 12288 && nt <= 2 &&
+  // launch and the partials: T takes 4.4 us and 0.5 us (16 ranks) or 0.85 us (32)
+  // for 1024 values of k while all workgroups run at once; two launches 6.5 to 8
+  // us in a graph, 2 more without. n = 4096: 1 row of rank 8, k = 1024 4.9 against
+  // 6.5, k = 4096 6.5 against 6.7; rank 32, k = 1024 6.3 against 7.2, k = 4096 8.8
+  // against 7.3; k = 14336, rank 8 12.3 against 8.3. Blocks of one tile, each its
+  // own adapter's, gain up to two workgroups a CU (64 rows of 48 adapters, 6144
+  // columns 11.4 against 15.4 us), larger blocks up to one (512 rows of 4
+  // adapters 13.0 against 10.7).
+  a->fused = (nt + 1) * (int64_t)a->k <= 8192 && nt <= 2 &&
              tiles * chunks_of(*a, kFusedWaves * kUnit) <= (a->block_m == 16 ? 640 : 256);
   // Parts of K: 512 workgroups (two a CU) where there is that much, each wave
   // with two steps of 64 at least.
@@ -788,7 +792,12 @@ void lora_choose(LoraArgs* a) {
   // Units of columns a workgroup: each adds up T anew, split * rank_pad * 256
   // bytes for 64 rows, beside 32 KB of a unit's Y there and back; so more units
   // the more there is to add up, while 256 workgroups are left, and more while
-  // 1024 are (few rows: four waves of one unit, and 2048).
+  // 1024 are (4096 rows, rank 32, k = n = 4096: 30.5 us with one unit, 26.7 so). Few
+  // rows: a unit for each of four waves, more while 768 workgroups are left (16
+  // rows of as many adapters, 28672 columns: 10.6 us with one unit, 9.1 so).
+  // 64 rows at once, Y by whole lines, from 64-row blocks on: 4096 rows of rank
+  // 16, k = 4096, n = 28672 144 against 112 us, rank 64, n = 4096 40 against 35
+  // (more than 64 ranks are more registers than hold the next unit's B and Y).
   a->wide = tiles_per_group(a->block_m) == 4 && a->rank_pad <= 64;
   if (a->wide) {
     const int64_t all = tiles / 4 * chunks_of(*a, kWide), t = (a->split * a->rank_pad + 127) / 128;
