@@ -450,3 +450,30 @@ def test_stream_and_weights_far_apart(qdg):
         torch.cuda.synchronize()
         _, bits = layer.norm(r, weight=H.to_f64(cw), bias=b if bias else None, r_f32=True)
         out.check(bits)
+
+
+@pytest.mark.parametrize("n", [3, 13, 1001, 2047, 4099, 8191, 16387])
+@pytest.mark.parametrize("wf32", [False, True])
+def test_cut_rows_with_tiny_ends(qdg, n, wf32):
+    """The last chunk of a row of an odd length holds zeros, subnormal and tiny values, or nothing but those."""
+    rng = np.random.default_rng(n)
+    ends = np.array([0.0, -0.0, 1e-40, -3e-39, 2.0 ** -100, 2.0 ** -101, 1.5 * 2.0 ** -126], np.float32)
+    x = rng.standard_normal((4, n)).astype(np.float32)
+    for row in range(3):
+        k = min(n, (n % 8, 1, 7)[row])
+        x[row, n - k:] = rng.permutation(ends)[:k]
+    x[3] = rng.choice(ends, n)
+    wt = torch.float32 if wf32 else torch.bfloat16
+    w, b = (torch.from_numpy(rng.standard_normal(n).astype(np.float32)).to(wt) for _ in range(2))
+    dx, dw, db = torch.from_numpy(x).cuda(), w.cuda(), b.cuda()
+    for kind, bias in (("rms", False), ("rms", True), ("layer", False)):
+        _, bits = layer.norm(x.astype(np.float64), None, None, None, w.double().numpy(), b.double().numpy() if bias else None,
+                             kind == "layer", 1e-30, 1.0, 0.0, True)
+        out = Out(4, n, "int8", True)
+        cfg = q.norm(n, kind=q.QDG_NORM_LAYER if kind == "layer" else q.QDG_NORM_RMS, xtype=q.QDG_O_F32, rtype=q.QDG_O_F32,
+                     wtype=q.QDG_O_F32 if wf32 else q.QDG_O_BF16, quant=q.QDG_Q_INT8, eps=1e-30, ldq=out.ldq)
+        rows, qa, sc, _ = out.args()
+        q.qdg_norm(cfg, dx.data_ptr(), None, None, None, None, dw.data_ptr(), _ptr(db if bias else None), 4, None, rows, qa,
+                   sc, None, q.current_stream())
+        torch.cuda.synchronize()
+        out.check(bits)
