@@ -757,9 +757,10 @@ qdg_status qdg_gated_act(const qdg_gated_config* cfg, const void* Y, int64_t M, 
    otype BF16 or F32, row stride ldy. All aligned to their elements.
    Products of bf16 numbers are exact in binary32 and are added there; the
    inner sums enter the second product, scaled, with 16 bits of their
-   significand (2^-18 of their value); the sum joins Y in binary32 and is
-   rounded once to otype. Results do not depend on other rows' values, but their
-   last bits may on M and the grouping (the order of the inner sums).
+   significand (2^-18 of their value; F32 Y: 24 bits, 2^-27); the sum joins Y in
+   binary32 and is rounded once to otype. Results do not depend on other rows'
+   values, but their last bits may on M and the grouping (the order of the inner
+   sums).
    n, k in [1, 2^20]; rank 1..256; num_slices 1..4, slice_end ascending, the
    last one n; num_adapters 1..1024; M in [0, 2^20] (0 enqueues nothing);
    block_m 16, 32, 64 or 128: the smaller while adapters hold few rows each
