@@ -539,47 +539,62 @@ __device__ __forceinline__ void row_stats(Raw8<F32> (&v)[CH], int n, int t, bool
 
 // What is absent is neutral: a factor 1, a term -0 (which leaves a sum its sign).
 // The new stream of eight values: residual_scale * r + gate * t. Without a norm
-// of x and with a product of at most 16 significant bits (short), that is one
-// rounding of binary32.
+// of x and with a product of at most 16 significant bits (short; a gate beside
+// bf16 x and weights only), that is one rounding of binary32, where no product
+// of the eight leaves binary32's normal range (or is 0).
 template <bool PLAIN, bool XF, bool RF, bool WF, bool EVEN>
 __device__ __forceinline__ Raw8<RF> join8(const NormArgs& a, const Raw8<XF>& x, const Raw8<RF>& r, const Raw8<WF>& g, int i,
                                           double mean, double rs) {
   const int n = a.n;
   const float scale = a.residual ? a.residual_scale : -1.0f;  // of zeros
-  float v[8];
-  if (PLAIN || a.short_join) {
-    if (a.gate) {
+  Raw8<RF> s;
+  auto put = [&](int j, float lo, float hi) {  // values 2 j and 2 j + 1
+    if constexpr (RF) {
+      s.d[2 * j] = __builtin_bit_cast(uint32_t, lo);
+      s.d[2 * j + 1] = __builtin_bit_cast(uint32_t, hi);
+    } else {
+      s.d[j] = to_bf16_pair(lo, hi);
+    }
+  };
+  bool open = !(PLAIN || a.short_join);
+  if (!open) {
+    if (!XF && !WF && a.gate) {
+      float least = __builtin_inff(), most = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(scale, r[j], x[j] * g[j]);
+      for (int j = 0; j < 4; ++j) {
+        const float p = x[2 * j] * g[2 * j], p1 = x[2 * j + 1] * g[2 * j + 1];
+        least = least3(least, p, p1);
+        most = fmaxf(fmaxf(most, fabsf(p)), fabsf(p1));
+        put(j, __builtin_fmaf(scale, r[2 * j], p), __builtin_fmaf(scale, r[2 * j + 1], p1));
+      }
+      open = !(least >= 0x1p-126f && most < __builtin_inff());
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(scale, r[j], x[j]);
-    }
-  } else {
-    Raw8<WF> w = load_vec8<WF, EVEN>(a.post_weight, 1.0f, i, n), b = load_vec8<WF, EVEN>(a.post_bias, -0.0f, i, n);
-    settle8<EVEN>(w, i, n);
-    settle8<EVEN>(b, i, n);
-    const double offset = a.post_weight ? (double)a.weight_offset : 0.0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      double d = ((double)x[j] - mean) * rs * ((double)w[j] + offset) + (double)b[j];
-      d = __builtin_fma((double)scale, (double)r[j], d * (double)g[j]);
-      v[j] = (float)d;
-      if (j & 1) one_at_a_time();
-    }
-    const int rest = n - i;
-    if (!EVEN && rest < 8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < rest ? v[j] : 0.f;
+      for (int j = 0; j < 4; ++j) put(j, __builtin_fmaf(scale, r[2 * j], x[2 * j]), __builtin_fmaf(scale, r[2 * j + 1], x[2 * j + 1]));
     }
   }
-  Raw8<RF> s;
-  if constexpr (RF) {
+  if (open) {
+    Raw8<WF> w, b;
+    if (!PLAIN) {
+      w = load_vec8<WF, EVEN>(a.post_weight, 1.0f, i, n);
+      b = load_vec8<WF, EVEN>(a.post_bias, -0.0f, i, n);
+      settle8<EVEN>(w, i, n);
+      settle8<EVEN>(b, i, n);
+    }
+    const double offset = a.post_weight ? (double)a.weight_offset : 0.0;
+    const int rest = n - i;
+    float v[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s.d[j] = __builtin_bit_cast(uint32_t, v[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s.d[j] = to_bf16_pair(v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < 8; ++j) {
+      double d = (double)x[j];
+      if (!PLAIN) d = (d - mean) * rs * ((double)w[j] + offset) + (double)b[j];
+      d = __builtin_fma((double)scale, (double)r[j], d * (double)g[j]);
+      v[j & 1] = EVEN || j < rest ? (float)d : 0.f;
+      if (j & 1) {
+        put(j >> 1, v[0], v[1]);
+        one_at_a_time();
+      }
+    }
   }
   return s;
 }
