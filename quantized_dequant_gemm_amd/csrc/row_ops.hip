@@ -604,8 +604,8 @@ __device__ __forceinline__ Raw8<RF> join8(const NormArgs& a, const Raw8<XF>& x, 
 // Not PLAIN (a bias or a mean): m = ((s - mean) rs) w, the mean in two binary32
 // parts, y = m + b; m's error, with two more roundings, and the sum's are within
 // 2^-21 |m| + 2^-23 |b| + 2^-44 |mean rs w|, and the roundings of both ends of
-// that interval are compared. Where (s - mean) rs or y is below 2^-100, or rs
-// leaves the middle of binary32's range, binary64 decides.
+// that interval are compared. Where (s - mean) rs or y is below 2^-100, rs
+// leaves the middle of binary32's range or w + offset may leave it, binary64 decides.
 template <bool PLAIN, bool RF, bool WF, bool EVEN>
 __device__ __forceinline__ Raw8<false> norm8(const NormArgs& a, const Raw8<RF>& s, const Raw8<WF>& w, const Raw8<WF>& b, int i,
                                              double mean, double rs, bool in_range) {
@@ -734,7 +734,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, MODE == kPlain && TPR <= 256
     }
     if (!a.out.rows && a.out.quant == QDG_Q_NONE) continue;
     row_stats<TPR, CH, RF>(s, n, t, !PLAIN && a.layer, a.eps, a.inv_n, mean, rs, buf, turn);
-    const bool in_range = rs > 0x1p-60 && rs < 0x1p60;
+    // an offset below 2^100 keeps any weight inside binary32's range
+    const bool in_range = rs > 0x1p-60 && rs < 0x1p60 && fabsf(a.weight_offset) < 0x1p100f;
     Raw8<false> o[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {

@@ -72,3 +72,21 @@ def test_gate_products_outside_binary32s_range(qdg, n, rf32):
             np.testing.assert_array_equal(new, s)
             np.testing.assert_array_equal(out.row_bits()[:5], bits[:5])
             _same_codes(out)
+
+
+@pytest.mark.parametrize("n", [1024, 1001])
+@pytest.mark.parametrize("wf32", [False, True])
+def test_weights_with_an_offset_past_binary32s_range(qdg, n, wf32):
+    """weight + offset above the largest binary32 number beside values that bring the product back."""
+    rng = np.random.default_rng(n)
+    x = rng.standard_normal((4, n)) * 2.0 ** -6
+    x[:, ::16] *= 2.0 ** 9
+    w = rng.standard_normal(n)
+    w[::2] = 3e38
+    w[1::8] = -3e38
+    for kind, bias in (("rms", None), ("rms", rng.standard_normal(n)), ("layer", None)):
+        out, new, s, bits = _call(x, False, "int8_zp", weight=w, bias=bias, wf32=wf32, kind=kind, offset=3e38)
+        np.testing.assert_array_equal(new, s)
+        assert (bits[:, 2::16] & 0x7FFF < 0x7F80).any()
+        np.testing.assert_array_equal(out.row_bits(), bits)
+        _same_codes(out)
