@@ -487,7 +487,9 @@ __device__ __forceinline__ double inverse_root(double x) {
   return y;
 }
 
-// 1 / sqrt(mean of squares + eps) of the row v, and with LAYER its mean. The
+// 1 / sqrt(mean of squares + eps) of the row v, and with LAYER its mean: s / n as
+// s inv_n and a step of Newton's iteration, which is exact where the quotient
+// is, so that a constant row (its sum is exact) has its value as mean. The
 // variance is the mean of squares less the mean's square, which keeps 46 bits
 // unless the mean is more than four deviations off 0; a row that lies further
 // off is summed again around its mean.
@@ -514,7 +516,11 @@ __device__ __forceinline__ void row_stats(Raw8<F32> (&v)[CH], int n, int t, bool
     }
     v[c].renew();
   }
-  if (layer) mean = row_sum<TPR>(s, buf, turn) * inv_n;
+  if (layer) {
+    s = row_sum<TPR>(s, buf, turn);
+    mean = s * inv_n;
+    mean = __builtin_fma(__builtin_fma(-mean, (double)n, s), inv_n, mean);
+  }
   double var = row_sum<TPR>(sq, buf, turn) * inv_n;
   if (layer) {
     var -= mean * mean;

@@ -90,3 +90,30 @@ def test_weights_with_an_offset_past_binary32s_range(qdg, n, wf32):
         assert (bits[:, 2::16] & 0x7FFF < 0x7F80).any()
         np.testing.assert_array_equal(out.row_bits(), bits)
         _same_codes(out)
+
+
+@pytest.mark.parametrize("n", [49, 196, 1001, 3136, 7488, 8191, 24500])
+def test_layer_norm_of_constant_rows(qdg, n):
+    """A row of one value has that value as its mean (n of them add up without a rounding), so it is 0 beside eps > 0 and
+    0 / 0 beside eps = 0."""
+    values = np.array([1.0, -3.140625, 0.1, 1e15, 1.1754944e-38, 7.0 / 3.0, -2e30])
+    x = np.tile(values[:, None], (1, n))
+    rng = np.random.default_rng(n)
+    w, b = rng.standard_normal(n), rng.standard_normal(n)
+    quants = ["none", "int8", "int8_zp"] + ["fp8"] * (n % 128 == 0) + ["mxfp4"] * (n % 32 == 0)
+    for i, quant in enumerate(quants):
+        for f32 in (False, True):
+            for bias in (None, b):
+                out, new, s, bits = _call(x, f32, quant, rf32=f32, weight=w, bias=bias, wf32=i == 2, kind="layer")
+                np.testing.assert_array_equal(new, s)
+                out.check(bits)
+            out, new, s, _ = _call(x, f32, quant, rf32=f32, weight=w, kind="layer", eps=0.0)
+            assert torch.isnan(out.rows()).all()
+    # the norm of x, as it joins the stream
+    for eps in (1e-5, 0.0):
+        out, new, s, bits = _call(x, True, "int8", rng.standard_normal(x.shape), True, weight=w, kind="layer", post=(w, b), eps=eps)
+        if eps:
+            np.testing.assert_array_equal(new, s)
+            out.check(bits)
+        else:
+            assert np.isnan(new).all()
