@@ -940,8 +940,10 @@ hipError_t gated_shape(const GatedArgs& a, hipStream_t s) {
   if (a.n <= 8192) return go(gated_kernel<512, 2, YF, EVEN>, 512, 1, a, s);
   // 1024 threads: one row a CU, its registers' most in flight; 512 hold two rows,
   // which binary32 Y has no registers for (16 x 14336 6.4 against 7.2 us, 4096 x 14336 90 against 66)
-  if (a.n <= 16384 && (YF || a.M <= 256)) return go(gated_kernel<1024, 2, YF, EVEN>, 1024, 1, a, s);
-  if (a.n <= 16384) return go(gated_kernel<512, 4, YF, EVEN>, 512, 1, a, s);
+  if constexpr (!YF) {
+    if (a.n <= 16384 && a.M > 256) return go(gated_kernel<512, 4, YF, EVEN>, 512, 1, a, s);
+  }
+  if (a.n <= 16384) return go(gated_kernel<1024, 2, YF, EVEN>, 1024, 1, a, s);
   if (a.n <= 32768) return go(gated_kernel<1024, 4, YF, EVEN>, 1024, 1, a, s);
   return go(gated_kernel<1024, 8, YF, EVEN>, 1024, 1, a, s);
 }
