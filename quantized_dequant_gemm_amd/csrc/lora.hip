@@ -19,15 +19,6 @@
 namespace qdg {
 namespace {
 
-typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_2_t;
-typedef __attribute__((ext_vector_type(4), aligned(4))) uint32_t u32x4_4_t;
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
-
-__device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
-  const f32x2_t v = {lo, hi};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
-}
-
 // A value that is the same for all lanes, in a scalar register: what follows
 // from it is then computed once for the wave.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -35,12 +26,6 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 template <class T>
 __device__ __forceinline__ T scalar_load(const T* p) {
   return *(const __attribute__((address_space(4))) T*)p;
-}
-
-// A lane exchange of DPP within 16 lanes.
-template <int CTRL>
-__device__ __forceinline__ float dpp_f32(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
 }
 
 // Eight neighbouring bf16 values at any element.
@@ -618,13 +603,13 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
     f32x4_t v = sum[k * kSumRow + s * 64 + 32 * h + 16 * half + (l & 15)];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[j] += dpp_f32<0xB1>(v[j]);   // lanes that differ in bit 0
-      v[j] += dpp_f32<0x4E>(v[j]);   // bit 1
-      v[j] += dpp_f32<0x141>(v[j]);  // a mirror of eight: bit 2
+      v[j] += dpp<kXor1>(v[j]);     // lanes that differ in bit 0
+      v[j] += dpp<kXor2>(v[j]);     // bit 1
+      v[j] += dpp<kMirror8>(v[j]);  // a mirror of eight: bit 2
     }
     f32x4_t o;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = dpp_f32<0x140>(v[j]);  // a mirror of sixteen: the other half
+    for (int j = 0; j < 4; ++j) o[j] = dpp<kMirror16>(v[j]);  // a mirror of sixteen: the other half
     if ((i & 15) == 0) {
       float r[8] = {v.x, v.y, v.z, v.w, o.x, o.y, o.z, o.w};
 #pragma unroll

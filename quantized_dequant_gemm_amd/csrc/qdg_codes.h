@@ -1,13 +1,44 @@
 // Encoders of activation rows: the rules of qdg_quantize_act and
 // qdg_quantize_act_zp for the values that one lane holds, shared by the
 // quantizers and by the row operators that end in codes (whose codes are
-// therefore those of the quantizer over the same bf16 values, bit for bit).
+// therefore those of the quantizer over the same bf16 values, bit for bit);
+// and the bf16 pairs, unaligned loads and lane exchanges that the row operators
+// and the adapters share.
 #pragma once
 #include "qdg_device.h"
 
 namespace qdg {
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __builtin_bit_cast(float, h << 16); }
+
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+// A pair of binary32 values as bf16, round to nearest even (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
+// Sixteen bytes at any bf16 or binary32 element.
+typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_2_t;
+typedef __attribute__((ext_vector_type(4), aligned(4))) uint32_t u32x4_4_t;
+
+// Lane exchanges of DPP within 16 lanes: lanes differing in bit 0, bit 1, a
+// mirror of 8 (bit 2, once bits 0 and 1 agree) and of 16 lanes (bit 3).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(uint32_t, v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u));
+}
 
 // Value j of a run of bf16 pairs.
 __device__ __forceinline__ float bf16_pair(uint32_t pair, int j) {

@@ -18,12 +18,9 @@
 namespace qdg {
 namespace {
 
-typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_2_t;
-typedef __attribute__((ext_vector_type(4), aligned(4))) uint32_t u32x4_4_t;
 typedef __attribute__((ext_vector_type(2), aligned(2))) uint32_t u32x2_2_t;
 typedef __attribute__((ext_vector_type(2), aligned(4))) uint32_t u32x2_4_t;
 typedef __attribute__((aligned(2))) uint32_t u32_2_t;
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 
 // Eight values of one type as they are stored: bf16 pairs or binary32.
 template <bool F32>
@@ -167,12 +164,6 @@ __device__ __forceinline__ float least3(float a, float b, float c) {
   return r;
 }
 
-// A pair of binary32 values as bf16, round to nearest even (v_cvt_pk_bf16_f32).
-__device__ __forceinline__ uint32_t to_bf16_pair(float lo, float hi) {
-  const f32x2_t v = {lo, hi};
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
-}
-
 // Between binary64 values: their chains side by side would take the registers
 // that let another wave in.
 __device__ __forceinline__ void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }
@@ -189,24 +180,6 @@ __device__ __forceinline__ Raw8<F32> load_vec8(const void* p, float absent, int 
 }
 
 // ------------------------------------------------------------------ reductions over the TPR threads of a row
-// Lane exchanges of DPP within 16 lanes: lanes differing in bit 0, bit 1, a
-// mirror of 8 (bit 2, once bits 0 and 1 agree) and of 16 lanes (bit 3).
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
-
-template <int CTRL>
-__device__ __forceinline__ double dpp(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u));
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(uint32_t, v)));
-}
-
 // Rows of 16 lanes, then halves of 32, against each other: of two copies of v
 // the swap leaves both rows (halves) in every lane.
 template <bool HALVES>
