@@ -188,9 +188,10 @@ __device__ __forceinline__ void load16(const uint16_t* x, int64_t i, int64_t k, 
 }
 
 // The codes of 16 values into q + i.
+template <bool BRANCH>
 __device__ __forceinline__ void encode16(const uint32_t (&v)[8], const ZpRow& z, int8_t* q, int64_t i, int64_t k) {
   uint32_t out[4];
-  encode_zp<8>(v, z, out);
+  encode_zp<8, BRANCH>(v, z, out);
   if (i + 16 <= k) {
     *(u32x4_t*)(q + i) = u32x4_t{out[0], out[1], out[2], out[3]};
   } else {
@@ -221,7 +222,7 @@ __device__ __forceinline__ void row_max2(uint32_t& a, uint32_t& b, uint32_t (&bu
 
 // CH > 0: a row of at most 16 TPR CH values in registers; CH = 0: any length,
 // read twice.
-template <int TPR, int CH>
+template <int TPR, int CH, bool BRANCH = false>
 __global__ __launch_bounds__(256) void act_int8_zp_kernel(const uint16_t* __restrict__ a, int64_t lda, int64_t M,
                                                           int64_t k, int8_t* __restrict__ q, int64_t ldq,
                                                           float* __restrict__ scales, int32_t* __restrict__ zeros) {
@@ -277,13 +278,13 @@ __global__ __launch_bounds__(256) void act_int8_zp_kernel(const uint16_t* __rest
     if constexpr (CH > 0) {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        if ((int64_t)(c * TPR + t) * 16 < k) encode16(v[c], z, y, (int64_t)(c * TPR + t) * 16, k);
+        if ((int64_t)(c * TPR + t) * 16 < k) encode16<BRANCH>(v[c], z, y, (int64_t)(c * TPR + t) * 16, k);
     } else {
       for (int c = 0; c < chunks; ++c) {
         const int64_t i = ((int64_t)c * TPR + t) * 16;
         if (i >= k) break;
         load16(x, i, k, v[0]);
-        encode16(v[0], z, y, i, k);
+        encode16<BRANCH>(v[0], z, y, i, k);
       }
     }
   }
@@ -299,8 +300,12 @@ hipError_t launch_quantize_act_zp(const void* a, int64_t lda, int64_t M, int64_t
                        (const uint16_t*)a, lda, M, k, qa, ldq, scales, zeros);
     return hipGetLastError();
   };
-  if (k <= 1024) return go(act_int8_zp_kernel<64, 1>, 4);
-  if (k <= 4096) return go(act_int8_zp_kernel<256, 1>, 1);
+  // From 8 workgroups a CU on the instructions of short rows count, before the
+  // latency of one (4096 x 4096 15.3 against 16.8 us, 2048 x 4096 9.3 against 9.4;
+  // 333 x 4096 4.3 against 4.1, 1 x 4096 3.5 against 3.1, 4096 x 1024 5.7 against
+  // 5.6); longer rows take the same time either way.
+  if (k <= 1024) return M >= 8192 ? go(act_int8_zp_kernel<64, 1, true>, 4) : go(act_int8_zp_kernel<64, 1>, 4);
+  if (k <= 4096) return M >= 2048 ? go(act_int8_zp_kernel<256, 1, true>, 1) : go(act_int8_zp_kernel<256, 1>, 1);
   if (k <= 8192) return go(act_int8_zp_kernel<256, 2>, 1);
   if (k <= 16384) return go(act_int8_zp_kernel<256, 4>, 1);
   return go(act_int8_zp_kernel<256, 0>, 1);

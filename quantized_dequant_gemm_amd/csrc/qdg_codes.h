@@ -153,8 +153,10 @@ __device__ __forceinline__ ZpRow zp_row(float lo, float hi) {
   return z;
 }
 
-// The codes of ND bf16 pairs.
-template <int ND>
+// The codes of ND bf16 pairs. BRANCH: binary64 behind a branch, one value at a
+// time, which takes fewer registers and instructions; else for all values side
+// by side and chosen afterwards, which is shorter for a row by itself.
+template <int ND, bool BRANCH>
 __device__ __forceinline__ void encode_zp(const uint32_t (&v)[ND], const ZpRow& z, uint32_t (&out)[ND / 2]) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
   const int shift = (int)z.zero - 0x4B400000;
@@ -173,7 +175,7 @@ __device__ __forceinline__ void encode_zp(const uint32_t (&v)[ND], const ZpRow& 
       const float f = bf16_pair(v[j >> 1], j);
       const double d = f == f ? rint((double)f * z.inv) : 0.0;
       c[j] = (int)fmin(fmax(d + z.zero, -128.0), 127.0);
-      __builtin_amdgcn_sched_barrier(0);  // one chain at a time: registers
+      if constexpr (BRANCH) __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll

@@ -348,7 +348,7 @@ __device__ __forceinline__ void finish_row(const Raw8<false> (&o)[CH], int n, in
     for (int c = 0; c < CH; ++c)
       if ((c * TPR + t) * 8 < n) {
         uint32_t code[2];
-        encode_zp<4>(o[c].d, z, code);
+        encode_zp<4, true>(o[c].d, z, code);
         store_codes<EVEN>(q, (c * TPR + t) * 8, n, u32x2_t{code[0], code[1]});
       }
     return;

@@ -117,3 +117,32 @@ def test_layer_norm_of_constant_rows(qdg, n):
             out.check(bits)
         else:
             assert np.isnan(new).all()
+
+
+@pytest.mark.parametrize("M,k", [(2049, 1040), (2048, 4090), (8195, 500), (8192, 1024)])
+def test_zero_point_codes_do_not_depend_on_the_batch(qdg, M, k):
+    """Many short rows take another instance of the quantizer than few: the same codes, with infinities and NaN too."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(k)
+    lda, ldq = (k + 7) // 8 * 8, (k + 15) // 16 * 16
+    a = torch.randn((M, lda), generator=gen, device="cuda").to(torch.bfloat16)
+    a[3, 7], a[4, 1], a[5, k - 1] = float("inf"), float("nan"), -float("inf")
+    a[6], a[7] = 0.0, 2.5
+
+    def quantize(rows):
+        m = rows.shape[0]
+        qa = torch.zeros((m, ldq), dtype=torch.int8, device="cuda")
+        s, z = torch.zeros(m, device="cuda"), torch.zeros(m, dtype=torch.int32, device="cuda")
+        q.qdg_quantize_act_zp(rows.data_ptr(), lda, m, k, qa.data_ptr(), ldq, s.data_ptr(), z.data_ptr(), q.current_stream())
+        return qa, s, z
+
+    whole = quantize(a)
+    for at in range(0, M, 500):
+        part = quantize(a[at:at + 500])
+        for w, p in zip(whole, part):
+            assert torch.equal(w[at:at + 500], p)
+    bits = a[:40, :k].contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+    codes, scales, zeros = layer.codes(bits, "int8_zp")
+    np.testing.assert_array_equal(whole[0][:40, :k].cpu().numpy(), codes)
+    np.testing.assert_array_equal(whole[1][:40].cpu().numpy(), scales)
+    np.testing.assert_array_equal(whole[2][:40].cpu().numpy(), zeros)
