@@ -85,7 +85,7 @@ def lora(y, x, ids, a, b, slice_ends, ranks=None, scales=None):
     step, so that sums that cut instead of rounding are held too):
       T    products of bf16 numbers are exact; k of them added in blocks of 32
            and those in a chain: (k / 32 + 64) e of sum |x a|
-      T'   scaled (2^-24) and held with 16 bits (2^-18): 2^-17 of it
+      T'   scaled (2^-24) and held with all 24 bits: 2^-23 of it
       sum  2 R products in blocks of 32 and a chain: (R / 16 + 64) e of sum |T' b|
       Y    one addition, half a step: 2^-24 of |y| + |sum|."""
     y, x = np.asarray(y, np.float64).copy(), np.asarray(x, np.float64)
@@ -103,7 +103,7 @@ def lora(y, x, ids, a, b, slice_ends, ranks=None, scales=None):
                 bb = b[ad, j0:j1, :r].T
                 add = s * (t @ bb)
                 size = abs(s) * (np.abs(t) @ np.abs(bb))
-                err[np.ix_(rows, range(j0, j1))] = (abs(s) * (dt @ np.abs(bb)) + 2.0 ** -17 * size
+                err[np.ix_(rows, range(j0, j1))] = (abs(s) * (dt @ np.abs(bb)) + 2.0 ** -23 * size
                                                     + (r / 16 + 64) * e * size
                                                     + 2.0 ** -24 * (np.abs(y[rows, j0:j1]) + np.abs(add)))
                 y[rows, j0:j1] += add

@@ -7,9 +7,9 @@
 // `up` (few rows) or `wide` (many) adds them in order and meets B. For the
 // fewest rows `fused` does both. Few rows: bound by A, B and the chain of
 // dependent loads; many: by Y's way there and back. T enters the second product
-// as bf16 terms, T = hi + lo with an error of 2^-18 of T (binary32 Y: a third
-// term, 2^-27): 16 ranks are one 16 x 16 x 32 MFMA, hi in its first 16 K values,
-// lo in the others, the same B beside both.
+// with all its 24 bits, as three bf16 terms: 16 ranks are two 16 x 16 x 32 MFMAs,
+// one with the first term in 16 of its K values and the second in the others,
+// one with the third in 16, the same B beside all.
 //
 // ODD instances serve a rank that is no multiple of 8 or a k that is none of 64:
 // their loads may end behind a row, or a tensor.
@@ -291,25 +291,26 @@ __device__ __forceinline__ void subtract(float (&v)[8], const u32x4_t& r) {
   for (int j = 0; j < 8; ++j) v[j] = rest(v[j], bf16_pair(d[j >> 1], j));
 }
 
-// Eight ranks of a row of T as terms, in the places of the MFMA's operand:
-// hi for lane groups 0 and 1, lo for 2 and 3; a third operand with YF.
-template <bool YF>
-constexpr int kTerms = YF ? 2 : 1;
-template <bool YF>
-__device__ __forceinline__ void store_terms(u32x4_t* t, float (&v)[8]) {
-  t[0] = bf16x8(v);
-  subtract(v, t[0]);
-  t[32] = bf16x8(v);
-  if constexpr (YF) {
-    subtract(v, t[32]);
-    t[64] = bf16x8(v);
-    t[96] = u32x4_t{0, 0, 0, 0};
-  }
+// Eight ranks of a row of T as terms, in the places of the MFMAs' operands: the
+// first for lane groups 0 and 1, the second for 2 and 3; the third for 0 and 1,
+// one place of zeros for 2 and 3.
+constexpr int kTerms = 97;
+__device__ __forceinline__ void store_terms(u32x4_t* t, int l, float (&v)[8]) {
+  t[l] = bf16x8(v);
+  subtract(v, t[l]);
+  t[32 + l] = bf16x8(v);
+  subtract(v, t[32 + l]);
+  t[64 + l] = bf16x8(v);
+  if (l == 0) t[96] = u32x4_t{0, 0, 0, 0};
+}
+__device__ __forceinline__ int third_place() {
+  const int lane = threadIdx.x & 63;
+  return lane < 32 ? 64 + lane : 96;
 }
 
 // The terms of MT tiles' T for one slice, from the partials: terms
-// [MT][steps][kTerms][64]. A thread adds eight ranks of one row over the parts.
-template <int MT, bool YF>
+// [MT][steps][kTerms]. A thread adds eight ranks of one row over the parts.
+template <int MT>
 __device__ __forceinline__ void terms_of(const LoraArgs& a, const Adapter& ad, int tile0, int tiles, int slice, int steps,
                                          u32x4_t* terms) {
   const int per = a.rank_pad / 16, groups = a.num_slices * per;
@@ -342,7 +343,7 @@ __device__ __forceinline__ void terms_of(const LoraArgs& a, const Adapter& ad, i
     float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = s * 16 + h * 8 + j < ad.rank ? v[j] * scale : 0.f;
-    store_terms<YF>(terms + (m * steps + s) * kTerms<YF> * 64 + l, v);
+    store_terms(terms + (m * steps + s) * kTerms, l, v);
   }
 }
 
@@ -469,17 +470,18 @@ struct BTile {
   }
 };
 
-template <int MT, bool YF>
+template <int MT>
 __device__ __forceinline__ void multiply_b(const u32x4_t (&bf)[4], const u32x4_t* terms, int steps, int s,
                                            f32x4_t (&acc)[MT][4]) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m) {
+    const u32x4_t* t = terms + (m * steps + s) * kTerms;
+    const u32x4_t tf = t[threadIdx.x & 63], third = t[third_place()];
 #pragma unroll
-    for (int k = 0; k < kTerms<YF>; ++k) {
-      const u32x4_t tf = terms[((m * steps + s) * kTerms<YF> + k) * 64 + (threadIdx.x & 63)];
+    for (int u = 0; u < 4; ++u) acc[m][u] = mfma_bf16(bf[u], tf, acc[m][u]);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) acc[m][u] = mfma_bf16(bf[u], tf, acc[m][u]);
-    }
+    for (int u = 0; u < 4; ++u) acc[m][u] = mfma_bf16(bf[u], third, acc[m][u]);
+  }
 }
 
 // A workgroup's columns: `width` of them (or fewer) in one slice.
@@ -504,7 +506,7 @@ __device__ __forceinline__ Columns columns_of(const LoraArgs& a, int chunk, int 
 template <int MT, bool YF, bool ODD>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int tiles) {
   const int span = a.span;
-  extern __shared__ u32x4_t terms[];  // [MT][rank step][hi, lo and, with YF, the third][64]
+  extern __shared__ u32x4_t terms[];  // [MT][rank step][kTerms]
   const int group = tile_group(a, MT);
   if (group < 0 || group * MT >= tiles) return;
   const int tile0 = group * MT;
@@ -527,7 +529,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int tiles) {
     old.load(a, row, col0 + 16 * c, cs.j1 - col0 - 16 * c);
   };
   if (col0 < cs.j1) ask();
-  terms_of<MT, YF>(a, ad, tile0, tiles, cs.slice, steps, terms);
+  terms_of<MT>(a, ad, tile0, tiles, cs.slice, steps, terms);
   __syncthreads();
   for (int unit = wave; unit < span && col0 < cs.j1; unit += 4) {
     if (unit != wave) ask();
@@ -539,7 +541,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int tiles) {
         b.load(a);
       }
       now.settle(a);
-      multiply_b<MT, YF>(now.v, terms, steps, s, acc);
+      multiply_b<MT>(now.v, terms, steps, s, acc);
     }
     old.add_and_store(a, row, col0 + 16 * c, cs.j1 - col0 - 16 * c, acc);
     col0 += 4 * kUnit;
@@ -560,7 +562,7 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
   // a wave's row of sums is 16 bytes longer, so that eight threads that add one value find it in eight places
   constexpr int kSumRow = NT * 64 + 1, kIn = kFusedWaves * (1 + NT) * kTileBytes / 16;
   __shared__ u32x4_t lds[kIn > kFusedWaves * kSumRow ? kIn : kFusedWaves * kSumRow];
-  __shared__ u32x4_t terms[NT * kTerms<YF> * 64];
+  __shared__ u32x4_t terms[NT * kTerms];
   // a tile's workgroups are on one XCD, whose L2 holds the adapter for all, while that has the CUs (grid_x)
   const int tile = blockIdx.x;
   if (tile >= tiles) return;
@@ -614,7 +616,7 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
       float r[8] = {v.x, v.y, v.z, v.w, o.x, o.y, o.z, o.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[j] = s * 16 + h * 8 + j < ad.rank ? r[j] * scale : 0.f;
-      store_terms<YF>(terms + s * kTerms<YF> * 64 + l, r);
+      store_terms(terms + s * kTerms, l, r);
     }
   }
   __syncthreads();
@@ -624,7 +626,7 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
   for (int s = 0; s < NT; ++s) {
     if (s >= steps) break;
     b[s].settle(a);
-    multiply_b<1, YF>(b[s].v, terms, steps, s, acc);
+    multiply_b<1>(b[s].v, terms, steps, s, acc);
   }
   old.add_and_store(a, row, col, cs.j1 - col, acc);
 }
@@ -645,9 +647,12 @@ constexpr int kWide = 128, kBStep = kWide * 32 + kWide / 8 * 16;
 template <int STEPS, bool YF, bool ODD>
 __global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_kernel(LoraArgs a, int tiles) {
   const int span = a.span;
-  __shared__ u32x4_t terms[4 * STEPS * kTerms<YF> * 64];
-  __shared__ u32x4_t lds[2][STEPS * kBStep / 16];
+  // one side with four steps: 42 KB let a third workgroup in (4096 rows, rank 64 35.6 against 36.7 us)
+  constexpr int kSides = STEPS == 4 ? 1 : 2;
+  __shared__ u32x4_t terms[4 * STEPS * kTerms];
+  __shared__ u32x4_t lds[kSides][STEPS * kBStep / 16];
   constexpr int kP = YF ? 2 : 1, kE = YF ? 4 : 8;  // pieces of a lane's row, elements a piece
+  constexpr int kB = YF ? 8 : STEPS == 2 ? 2 : 4;  // column tiles at a time, as many as registers hold
   const int group = tile_group(a, 4);
   if (group < 0 || group * 4 >= tiles) return;
   const int tile0 = group * 4;
@@ -698,7 +703,7 @@ __global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_ke
   };
   load_b(0);
   load_y(0);
-  terms_of<4, YF>(a, ad, tile0, tiles, cs.slice, steps, terms);
+  terms_of<4>(a, ad, tile0, tiles, cs.slice, steps, terms);
   put_b(0);
   __syncthreads();
   for (int unit = 0; unit < units; ++unit) {
@@ -713,18 +718,22 @@ __global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_ke
       load_y(unit + 1);
     }
     f32x4_t acc[8] = {};
-    const char* bl = (const char*)lds[unit & 1] + (YF ? q * 128 + (q >> 1) * 16 : q * 272) + (c & 1) * 16;
+    const char* bl = (const char*)lds[unit & (kSides - 1)] + (YF ? q * 128 + (q >> 1) * 16 : q * 272) + (c & 1) * 16;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       if (s >= steps) break;
+      const u32x4_t* tt = terms + (wave * steps + s) * kTerms;
+      const u32x4_t tf = tt[lane], third = tt[third_place()];
 #pragma unroll
-      for (int k = 0; k < kTerms<YF>; ++k) {
-        const u32x4_t tf = terms[((wave * steps + s) * kTerms<YF> + k) * 64 + lane];
+      for (int g = 0; g < 8; g += kB) {
+        u32x4_t bf[kB];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const u32x4_t bf = *(const u32x4_t*)(bl + s * kBStep + (YF ? (u >> 2) * 8 * 272 + (u & 3) * 32 : u * 32));
-          acc[u] = mfma_bf16(tf, bf, acc[u]);
-        }
+        for (int u = 0; u < kB; ++u)
+          bf[u] = *(const u32x4_t*)(bl + s * kBStep + (YF ? (g + u) / 4 * 8 * 272 + (g + u) % 4 * 32 : (g + u) * 32));
+#pragma unroll
+        for (int u = 0; u < kB; ++u) acc[g + u] = mfma_bf16(tf, bf[u], acc[g + u]);
+#pragma unroll
+        for (int u = 0; u < kB; ++u) acc[g + u] = mfma_bf16(third, bf[u], acc[g + u]);
       }
     }
     const int col0 = cs.j0 + unit * kWide;
@@ -742,7 +751,8 @@ __global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_ke
         else store_elements<YF>(a.Y, row[i] + col0 + 64 * p, cut, v);
       }
     }
-    if (more) put_b((unit + 1) & 1);
+    if (kSides == 1) __syncthreads();
+    if (more) put_b((unit + 1) & (kSides - 1));
     __syncthreads();
   }
 }
@@ -861,7 +871,7 @@ hipError_t two(const LoraArgs& a, hipStream_t s) {
     if (a.rank_pad == 16) return wide<ODD, 1>(a, grid, tiles, s);
     return a.rank_pad == 32 ? wide<ODD, 2>(a, grid, tiles, s) : wide<ODD, 4>(a, grid, tiles, s);
   }
-  const size_t lds = (size_t)LT * (a.rank_pad / 16) * (a.yf32 ? 2 : 1) * 64 * sizeof(u32x4_t);
+  const size_t lds = (size_t)LT * (a.rank_pad / 16) * kTerms * sizeof(u32x4_t);
   auto kernel = a.yf32 ? lora_up_kernel<LT, true, ODD> : lora_up_kernel<LT, false, ODD>;
   hipLaunchKernelGGL(kernel, grid, dim3(256), lds, s, a, (int)tiles);
   return hipGetLastError();

@@ -1,0 +1,73 @@
+"""qdg_lora: values at which the inner sums' way into the second product shows. Every case runs through the kernel that
+does both products, the one for few rows and the one for many, each with and without cut loads."""
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_dequant_gemm_amd as q
+from tests import gpu_helpers as H
+from tests.test_gpu_lora import Group, _ptr
+
+pytestmark = pytest.mark.gpu
+
+# (rows, block_m, k): one launch; two launches with few rows; with 64 rows at once
+PATHS = {"fused": (5, 16, 128), "fused cut": (5, 16, 72), "up": (20, 16, 4224), "up cut": (20, 16, 4168),
+         "wide": (70, 64, 4224), "wide cut": (70, 64, 4168)}
+
+
+def _bf16(x):
+    with np.errstate(over="ignore"):
+        return torch.from_numpy(np.ascontiguousarray(x, np.float32)).cuda().to(torch.bfloat16)
+
+
+def _lora(path, x, a, b, y, f32, scales=None):
+    """x [k'], a [R][k'], b [n][R], y [n]: every row of the call is this one, k' filled up with zeros. Returns the rows."""
+    M, bm, k = PATHS[path]
+    rank, n = a.shape[0], b.shape[0]
+    full = np.zeros((M, k))
+    full[:, :x.size] = x
+    fa = np.zeros((1, 1, rank, k))
+    fa[0, 0, :, :x.size] = a
+    dx, da, db = _bf16(full), _bf16(fa), _bf16(b[None])
+    dy = torch.from_numpy(np.tile(np.asarray(y, np.float32), (M, 1))).cuda().to(torch.float32 if f32 else torch.bfloat16)
+    ds = None if scales is None else H.dev(np.asarray(scales, np.float32))
+    g = Group(np.zeros(M, np.int32), 1, bm)
+    cfg = q.lora(n, k, rank, otype=q.QDG_O_F32 if f32 else q.QDG_O_BF16)
+    nbytes = q.qdg_lora_workspace(cfg, M, bm)
+    assert (nbytes == 0) == path.startswith("fused")
+    ws = torch.full((max(16, nbytes),), 0xFF, dtype=torch.uint8, device="cuda")
+    q.qdg_lora(cfg, dx.data_ptr(), da.data_ptr(), db.data_ptr(), None, _ptr(ds), *g.args(), dy.data_ptr(), ws.data_ptr(),
+               nbytes, q.current_stream())
+    torch.cuda.synchronize()
+    got = H.to_f64(dy)
+    np.testing.assert_array_equal(got, np.tile(got[:1], (M, 1)))
+    return got[0]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("path", list(PATHS))
+def test_inner_sums_keep_all_bits_of_binary32(qdg, path, f32):
+    """T of 24 significant bits: Y is T times a power of two, and of two inner sums that differ in their last eight bits
+    only the difference, so that a lost, doubled or misplaced term of T shows."""
+    rng = np.random.default_rng(7)
+    n = 200
+    x = np.array([1.0, 2.0 ** -8, 2.0 ** -16])
+    for rank in (2, 8, 18, 34, 64):
+        if path.startswith("fused") and rank > 32:
+            continue
+        a = np.zeros((rank, 3))
+        r0, r1 = rng.choice(rank, 2, replace=False)
+        a[r0] = 2 * rng.integers(64, 128, 3) + 1  # 128 to 255, odd: every bit of the 24 counts
+        a[r1] = -a[r0, 0], -a[r0, 1], 0.0
+        t = a @ x
+        b = np.zeros((n, rank))
+        power = 2.0 ** rng.integers(-20, 20, n)
+        b[:, r0] = power
+        # one inner sum: exact in binary32; two additions inside the product, each off by a step at most
+        got = _lora(path, x, a, b, np.zeros(n), f32)
+        assert np.all(np.abs(got - t[r0] * power) <= (2.0 ** -22 + (0 if f32 else 2.0 ** -8)) * t[r0] * power)
+        # two that cancel: what is left has eight bits, and the sums on the way at most 24
+        b[:, r1] = power
+        got = _lora(path, x, a, b, np.zeros(n), f32)
+        np.testing.assert_array_equal(got, (t[r0] + t[r1]) * power)
