@@ -278,29 +278,29 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int tiles, i
 }
 
 // ------------------------------------------------------------------ the terms of T
-// What its bf16 rounding leaves of t; 0 where that is an infinity or NaN, which stands for itself.
-__device__ __forceinline__ float rest(float t, float rounded) {
-  return fabsf(rounded) < __builtin_inff() ? t - rounded : 0.f;
+// The bf16 numbers that binary32 values begin with; what is left of them is exact.
+__device__ __forceinline__ uint32_t head_pair(float lo, float hi) {
+  return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
 }
-__device__ __forceinline__ u32x4_t bf16x8(const float (&v)[8]) {
-  return u32x4_t{to_bf16_pair(v[0], v[1]), to_bf16_pair(v[2], v[3]), to_bf16_pair(v[4], v[5]), to_bf16_pair(v[6], v[7])};
-}
-__device__ __forceinline__ void subtract(float (&v)[8], const u32x4_t& r) {
-  const uint32_t d[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = rest(v[j], bf16_pair(d[j >> 1], j));
+__device__ __forceinline__ float tail(float t) {
+  return t - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, t) & 0xFFFF0000u);
 }
 
 // Eight ranks of a row of T as terms, in the places of the MFMAs' operands: the
 // first for lane groups 0 and 1, the second for 2 and 3; the third for 0 and 1,
-// one place of zeros for 2 and 3.
+// one place of zeros for 2 and 3. Each term is cut off, not rounded: none is
+// larger than T, so that no term or product of one overflows where T's does
+// not. An infinity or NaN (quiet, as a product's result) is its own first term,
+// with nothing left.
 constexpr int kTerms = 97;
 __device__ __forceinline__ void store_terms(u32x4_t* t, int l, float (&v)[8]) {
-  t[l] = bf16x8(v);
-  subtract(v, t[l]);
-  t[32 + l] = bf16x8(v);
-  subtract(v, t[32 + l]);
-  t[64 + l] = bf16x8(v);
+  t[l] = u32x4_t{head_pair(v[0], v[1]), head_pair(v[2], v[3]), head_pair(v[4], v[5]), head_pair(v[6], v[7])};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = fabsf(v[j]) < __builtin_inff() ? tail(v[j]) : 0.f;
+  t[32 + l] = u32x4_t{head_pair(v[0], v[1]), head_pair(v[2], v[3]), head_pair(v[4], v[5]), head_pair(v[6], v[7])};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = tail(v[j]);
+  t[64 + l] = u32x4_t{head_pair(v[0], v[1]), head_pair(v[2], v[3]), head_pair(v[4], v[5]), head_pair(v[6], v[7])};
   if (l == 0) t[96] = u32x4_t{0, 0, 0, 0};
 }
 __device__ __forceinline__ int third_place() {

@@ -71,3 +71,28 @@ def test_inner_sums_keep_all_bits_of_binary32(qdg, path, f32):
         b[:, r1] = power
         got = _lora(path, x, a, b, np.zeros(n), f32)
         np.testing.assert_array_equal(got, (t[r0] + t[r1]) * power)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("path", list(PATHS))
+def test_inner_sums_next_to_binary32s_largest(qdg, path, f32):
+    """Finite inner sums whose bf16 rounding would be infinite, and products that only the rounding would take past the
+    largest number."""
+    n = 130
+    # T = 2^128 - 2^104, the largest binary32 number, from three bf16 numbers
+    x, a = np.ones(3), np.array([[255 * 2.0 ** 120, 255 * 2.0 ** 112, 255 * 2.0 ** 104]])
+    b = 2.0 ** -np.arange(1.0, n + 1)[:, None]
+    want = (2.0 ** 128 - 2.0 ** 104) * b[:, 0]
+    got = _lora(path, x, a, b, np.zeros(n), f32)
+    # two additions inside the product, each off by a step at most; bf16 Y: half a step
+    assert np.all(np.abs(got - want) <= (2.0 ** -22 + (0 if f32 else 2.0 ** -8)) * want)
+    got = _lora(path, x, -a, b, np.zeros(n), f32, scales=[1.0])
+    assert np.all(np.abs(got + want) <= (2.0 ** -22 + (0 if f32 else 2.0 ** -8)) * want)
+    # T = 1 + 2^-8 + 2^-20 beside 255 2^120: 0.99998 of 2^128; T's nearest bf16 number 1 + 2^-7 would overflow
+    x, a = np.ones(3), np.array([[1.0, 2.0 ** -8, 2.0 ** -20]])
+    b = np.full((n, 1), 255 * 2.0 ** 120)
+    want = (1 + 2.0 ** -8 + 2.0 ** -20) * b[:, 0]
+    # bf16 Y: brought into its range by the Y that is there
+    y0 = 0.0 if f32 else -(2.0 ** 127)
+    got = _lora(path, x, a, b, np.full(n, y0), f32)
+    assert np.all(np.abs(got - (want + y0)) <= (2.0 ** -22 + (0 if f32 else 2.0 ** -8)) * want)
