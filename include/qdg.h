@@ -758,7 +758,8 @@ qdg_status qdg_gated_act(const qdg_gated_config* cfg, const void* Y, int64_t M, 
    Products of bf16 numbers are exact in binary32 and are added there; the
    inner sums enter the second product, scaled, with all 24 bits of their
    significand (of those below 2^-109 only what is above 2^-133); the sum joins
-   Y in binary32 and is rounded once to otype. Results do not depend on other rows'
+   Y in binary32 and is rounded once to otype. Infinities and NaN in X, A and
+   B go the way of IEEE arithmetic (ranks behind an adapter's own do not count). Results do not depend on other rows'
    values, but their last bits may on M and the grouping (the order of the inner
    sums).
    n, k in [1, 2^20]; rank 1..256; num_slices 1..4, slice_end ascending, the

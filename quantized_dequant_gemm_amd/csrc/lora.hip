@@ -470,7 +470,29 @@ struct BTile {
   }
 };
 
-template <int MT>
+// An infinite or NaN entry of B is to meet an inner sum's first term only: 0, a
+// rest of 0 or one of the other sign beside it would make its product a NaN. So
+// where a wave's sums hold a NaN it computes them again with finite_part(B)
+// beside the other terms: CAREFUL.
+__device__ __forceinline__ u32x4_t finite_part(u32x4_t v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] &= ((v[j] & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((v[j] & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
+  return v;
+}
+// Does any of a wave's sums hold a NaN? (The least magnitude of all does then.)
+template <int N>
+__device__ __forceinline__ bool any_nan(const f32x4_t (&acc)[N]) {
+  float m = 0.f;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    m = least3(m, acc[u].x, acc[u].y);
+    m = least3(m, acc[u].z, acc[u].w);
+  }
+  return __any(m != m);
+}
+
+template <int MT, bool CAREFUL>
 __device__ __forceinline__ void multiply_b(const u32x4_t (&bf)[4], const u32x4_t* terms, int steps, int s,
                                            f32x4_t (&acc)[MT][4]) {
 #pragma unroll
@@ -478,9 +500,12 @@ __device__ __forceinline__ void multiply_b(const u32x4_t (&bf)[4], const u32x4_t
     const u32x4_t* t = terms + (m * steps + s) * kTerms;
     const u32x4_t tf = t[threadIdx.x & 63], third = t[third_place()];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) acc[m][u] = mfma_bf16(bf[u], tf, acc[m][u]);
+    for (int u = 0; u < 4; ++u) {
+      const u32x4_t b = CAREFUL && (threadIdx.x & 32) ? finite_part(bf[u]) : bf[u];
+      acc[m][u] = mfma_bf16(b, tf, acc[m][u]);
+    }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) acc[m][u] = mfma_bf16(bf[u], third, acc[m][u]);
+    for (int u = 0; u < 4; ++u) acc[m][u] = mfma_bf16(CAREFUL ? finite_part(bf[u]) : bf[u], third, acc[m][u]);
   }
 }
 
@@ -541,7 +566,22 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int tiles) {
         b.load(a);
       }
       now.settle(a);
-      multiply_b<MT>(now.v, terms, steps, s, acc);
+      multiply_b<MT, false>(now.v, terms, steps, s, acc);
+    }
+    bool nan = false;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) nan |= any_nan(acc[m]);
+    if (nan) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[m][u] = f32x4_t{};
+      for (int s = 0; s < steps; ++s) {
+        b.place(a, ad, col0, cs.j1, s);
+        b.load(a);
+        b.settle(a);
+        multiply_b<MT, true>(b.v, terms, steps, s, acc);
+      }
     }
     old.add_and_store(a, row, col0 + 16 * c, cs.j1 - col0 - 16 * c, acc);
     col0 += 4 * kUnit;
@@ -626,7 +666,14 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
   for (int s = 0; s < NT; ++s) {
     if (s >= steps) break;
     b[s].settle(a);
-    multiply_b<1>(b[s].v, terms, steps, s, acc);
+    multiply_b<1, false>(b[s].v, terms, steps, s, acc);
+  }
+  if (any_nan(acc[0])) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) acc[0][u] = f32x4_t{};
+#pragma unroll
+    for (int s = 0; s < NT; ++s)
+      if (s < steps) multiply_b<1, true>(b[s].v, terms, steps, s, acc);
   }
   old.add_and_store(a, row, col, cs.j1 - col, acc);
 }
@@ -642,10 +689,13 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
 // way meanwhile. 4096 rows, 28672 columns of bf16, rank 16 86 us (5.0 TB/s of Y
 // there and back: HBM); 2048 rows, rank 64, 4096 columns 13 us (39 MB, 3.0 TB/s:
 // two rounds of workgroups). Four waves a SIMD where 128 registers hold a step
-// (gate-up 104 -> 97 us), three with four steps of B on their way.
+// (gate-up 104 -> 97 us), three with four steps of B on their way, two and no
+// more beside binary32 Y (gate-up of rank 16 195 against 204 us with three).
 constexpr int kWide = 128, kBStep = kWide * 32 + kWide / 8 * 16;
+template <int STEPS, bool YF>
+constexpr int kWideWaves = YF ? 2 : STEPS == 4 ? 3 : 4;
 template <int STEPS, bool YF, bool ODD>
-__global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_kernel(LoraArgs a, int tiles) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kWideWaves<STEPS, YF>, YF ? 2 : 8))) void lora_wide_kernel(LoraArgs a, int tiles) {
   const int span = a.span;
   // one side with four steps: 42 KB let a third workgroup in (4096 rows, rank 64 35.6 against 36.7 us)
   constexpr int kSides = STEPS == 4 ? 1 : 2;
@@ -661,12 +711,14 @@ __global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_ke
   const Columns cs = columns_of(a, blockIdx.y, span * kWide);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane >> 4, q = lane & 15;
   const int steps = (ad.rank + 15) / 16, units = min(span, (cs.j1 - cs.j0 + kWide - 1) / kWide);
-  int64_t row[4];  // of 4 c + i, as a place in Y; -1: padding
+  int row[4];  // of 4 c + i; -1: padding
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = row_at(a, (tile0 + wave) * 16 + 4 * c + i);
-    row[i] = r < 0 ? -1 : (int64_t)r * a.ldy + (YF ? 4 : 8) * q;
-  }
+  for (int i = 0; i < 4; ++i) row[i] = row_at(a, (tile0 + wave) * 16 + 4 * c + i);
+  // a row's place in Y, worked out anew each time: 64 bits of each row would be registers
+  auto place = [&](int i) {
+    asm volatile("" : "+v"(row[i]));
+    return (int64_t)row[i] * a.ldy + (YF ? 4 : 8) * q;
+  };
   // B: a thread has eight ranks of a column in each step
   const int bc = threadIdx.x >> 1, bh = threadIdx.x & 1;
   u32x4_t bin[STEPS];
@@ -692,14 +744,16 @@ __global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_ke
   auto load_y = [&](int unit) {
     const int col0 = cs.j0 + unit * kWide;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      if (row[i] < 0) continue;
+      const int64_t at = place(i) + col0;
 #pragma unroll
       for (int p = 0; p < kP; ++p) {
         const int cut = cs.j1 - col0 - 64 * p - kE * q;
-        if (row[i] < 0) continue;
-        if (cut >= kE) y[i][p] = load_piece<YF>(a.Y, row[i] + col0 + 64 * p, 0);
-        else y[i][p] = load_elements<YF>(a.Y, row[i] + col0 + 64 * p, cut);
+        if (cut >= kE) y[i][p] = load_piece<YF>(a.Y, at + 64 * p, 0);
+        else y[i][p] = load_elements<YF>(a.Y, at + 64 * p, cut);
       }
+    }
   };
   load_b(0);
   load_y(0);
@@ -736,10 +790,26 @@ __global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_ke
         for (int u = 0; u < kB; ++u) acc[g + u] = mfma_bf16(third, bf[u], acc[g + u]);
       }
     }
+    if (any_nan(acc)) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) acc[u] = f32x4_t{};
+      for (int s = 0; s < steps; ++s) {
+        const u32x4_t* tt = terms + (wave * steps + s) * kTerms;
+        const u32x4_t tf = tt[lane], third = tt[third_place()];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const u32x4_t bf = *(const u32x4_t*)(bl + s * kBStep + (YF ? u / 4 * 8 * 272 + u % 4 * 32 : u * 32)), fin = finite_part(bf);
+          acc[u] = mfma_bf16(tf, lane & 32 ? fin : bf, acc[u]);
+          acc[u] = mfma_bf16(third, fin, acc[u]);
+          __builtin_amdgcn_sched_barrier(0);  // one tile at a time: registers
+        }
+      }
+    }
     const int col0 = cs.j0 + unit * kWide;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (row[i] < 0) continue;
+      const int64_t at = place(i) + col0;
 #pragma unroll
       for (int p = 0; p < kP; ++p) {
         const int cut = cs.j1 - col0 - 64 * p - kE * q;
@@ -747,8 +817,8 @@ __global__ __launch_bounds__(256, YF ? 2 : STEPS == 4 ? 3 : 4) void lora_wide_ke
         u32x4_t v;
         if constexpr (YF) v = add_f32(was[i][p], s0);
         else v = add_bf16(was[i][p], s0, f32x4_t{acc[4][i], acc[5][i], acc[6][i], acc[7][i]});
-        if (cut >= kE) store_piece<YF>(a.Y, row[i] + col0 + 64 * p, 0, v);
-        else store_elements<YF>(a.Y, row[i] + col0 + 64 * p, cut, v);
+        if (cut >= kE) store_piece<YF>(a.Y, at + 64 * p, 0, v);
+        else store_elements<YF>(a.Y, at + 64 * p, cut, v);
       }
     }
     if (kSides == 1) __syncthreads();

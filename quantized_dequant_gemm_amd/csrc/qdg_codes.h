@@ -40,6 +40,13 @@ __device__ __forceinline__ double dpp(double v) {
   return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u));
 }
 
+// The least of three magnitudes; a NaN among them comes through.
+__device__ __forceinline__ float least3(float a, float b, float c) {
+  float r;
+  asm("v_minimum3_f32 %0, |%1|, |%2|, |%3|" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // Value j of a run of bf16 pairs.
 __device__ __forceinline__ float bf16_pair(uint32_t pair, int j) {
   return __builtin_bit_cast(float, j & 1 ? pair & 0xFFFF0000u : pair << 16);

@@ -157,13 +157,6 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int i, int n, u32x2_t 
   if (rest & 1) *p = (uint8_t)w;
 }
 
-// The least of three magnitudes; a NaN among them comes through.
-__device__ __forceinline__ float least3(float a, float b, float c) {
-  float r;
-  asm("v_minimum3_f32 %0, |%1|, |%2|, |%3|" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
-}
-
 // Between binary64 values: their chains side by side would take the registers
 // that let another wave in.
 __device__ __forceinline__ void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }

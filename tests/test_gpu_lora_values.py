@@ -96,3 +96,37 @@ def test_inner_sums_next_to_binary32s_largest(qdg, path, f32):
     y0 = 0.0 if f32 else -(2.0 ** 127)
     got = _lora(path, x, a, b, np.full(n, y0), f32)
     assert np.all(np.abs(got - (want + y0)) <= (2.0 ** -22 + (0 if f32 else 2.0 ** -8)) * want)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("path", list(PATHS))
+@pytest.mark.parametrize("rank", [1, 8, 20])
+def test_infinities_and_nan_in_b(qdg, path, f32, rank):
+    """An infinite entry of B makes its column infinite, with the sign of T times it; NaN, infinities of both signs and an
+    infinity beside T = 0 make it NaN. Other columns keep their values."""
+    rng = np.random.default_rng(rank)
+    n, k = 300, 72
+    for exact in (True, False):
+        # T that bf16 holds (nothing is left for its other terms), and any T
+        x, a = (np.ones(k), np.ones((rank, k))) if exact else (rng.standard_normal(k), rng.standard_normal((rank, k)))
+        a[-1] *= -1.0
+        b = rng.standard_normal((n, rank))
+        clean = b.copy()
+        b[3, 0], b[64, 0], b[130, rank - 1], b[299, rank - 1], b[17, 0] = np.inf, -np.inf, np.inf, -np.inf, np.nan
+        b[200, 0] = np.inf
+        b[200, rank - 1] = np.inf if (a @ x)[0] * (a @ x)[-1] < 0 else -np.inf
+        x64, a64, b64 = (H.to_f64(_bf16(v)) for v in (x, a, b))
+        y0 = rng.standard_normal(n).astype(np.float32) if f32 else H.to_f64(_bf16(rng.standard_normal(n)))
+        with np.errstate(invalid="ignore"):
+            want = y0 + ((a64 @ x64) * b64).sum(axis=1)
+        got = _lora(path, x, a, b, y0, f32)
+        bad = ~np.isfinite(want)
+        assert bad.sum() == 6
+        np.testing.assert_array_equal(got[bad], want[bad])
+        np.testing.assert_array_equal(got[~bad], _lora(path, x, a, clean, y0, f32)[~bad])
+    # T = 0: NaN; T infinite: an infinity
+    for first, result in ((0.0, np.nan), (np.inf, np.inf)):
+        b = np.ones((n, rank))
+        b[5] = np.inf
+        got = _lora(path, np.array([first]), np.ones((rank, 1)), b, np.zeros(n), f32)
+        np.testing.assert_array_equal(got[5], result)
