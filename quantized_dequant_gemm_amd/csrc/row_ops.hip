@@ -434,11 +434,14 @@ constexpr uint32_t kMiddle = (uint32_t)(2 * ULPS) << 16 | 0xFFFFu;
 
 // ------------------------------------------------------------------ norms
 // kPlain: an RMS norm of the stream with bf16 weights, no bias, a join that one
-// rounding of binary32 settles, and rows of whole chunks. kEven: anything else
+// rounding of binary32 settles, no gate, and rows of whole chunks. kPlainGate:
+// such a norm with a gate, whose check of the product's range takes registers
+// (without an instance of its own 4096 x 4096 with fp8 codes alone takes 29.9 us
+// instead of 26.8). kEven: anything else
 // with bf16 weights in rows of whole chunks. kGeneral: bf16 weights, a cut last
 // chunk. kF32Weights: any row (one more instance for whole chunks would bring
 // 4096 x 4096 from 48.8 to 47.3 us and 4096 x 8192 layer from 109 to 114).
-enum { kPlain, kEven, kGeneral, kF32Weights };
+enum { kPlain, kPlainGate, kEven, kGeneral, kF32Weights };
 
 // 1 / sqrt(x): v_rsq_f64 (2^-14 or better) and three steps of Newton's
 // iteration, each of which squares the error; 0 and infinity stay as they are.
@@ -514,7 +517,7 @@ __device__ __forceinline__ void row_stats(Raw8<F32> (&v)[CH], int n, int t, bool
 // of x and with a product of at most 16 significant bits (short; a gate beside
 // bf16 x and weights only), that is one rounding of binary32, where no product
 // of the eight leaves binary32's normal range (or is 0).
-template <bool PLAIN, bool XF, bool RF, bool WF, bool EVEN>
+template <bool PLAIN, bool GATE, bool XF, bool RF, bool WF, bool EVEN>
 __device__ __forceinline__ Raw8<RF> join8(const NormArgs& a, const Raw8<XF>& x, const Raw8<RF>& r, const Raw8<WF>& g, int i,
                                           double mean, double rs) {
   const int n = a.n;
@@ -530,7 +533,7 @@ __device__ __forceinline__ Raw8<RF> join8(const NormArgs& a, const Raw8<XF>& x, 
   };
   bool open = !(PLAIN || a.short_join);
   if (!open) {
-    if (!XF && !WF && a.gate) {
+    if (GATE && !XF && !WF && a.gate) {
       float least = __builtin_inff(), most = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -653,11 +656,12 @@ __device__ __forceinline__ Raw8<false> norm8(const NormArgs& a, const Raw8<RF>& 
 // it; 333 x 7168 norms on both sides 13.2 us (2.7 TB/s): one workgroup or two a
 // CU, each a chain of load, two sums with a barrier, stores; 1 x 4096 3.8 us in a
 // graph. Four waves a SIMD are 128 registers; kPlain in 256 threads has five in
-// 96 (4096 x 4096 fp8 27.3 against 28.1 us), in 512 not (4096 x 8192 62.4 against
-// 61.0: two workgroups a CU either way, and some spilled).
+// 96 (4096 x 4096 with fp8 codes alone 26.8 against 28.1 us, with a binary32
+// stream 37.5 against 38.7), in 512 not (4096 x 8192 62.4 against 61.0: two
+// workgroups a CU either way, and some spilled).
 template <int TPR, int CH, bool XF, bool RF, int MODE>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, MODE == kPlain && TPR <= 256 ? 5 : 4) void norm_kernel(NormArgs a) {
-  constexpr bool PLAIN = MODE == kPlain, WF = MODE == kF32Weights, EVEN = MODE == kPlain || MODE == kEven;
+  constexpr bool PLAIN = MODE == kPlain || MODE == kPlainGate, GATE = MODE != kPlain, WF = MODE == kF32Weights, EVEN = PLAIN || MODE == kEven;
   __shared__ Buffers buf;
   int turn = 0;
   constexpr int kThreads = TPR < 256 ? 256 : TPR, RPB = kThreads / TPR;
@@ -667,7 +671,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, MODE == kPlain && TPR <= 256
     if (TPR < 256 && row >= a.M) break;  // whole waves: no barrier below
     const char* x = (const char*)a.x + row * a.ldx * (XF ? 4 : 2);
     const char* r = (const char*)a.residual + row * a.ldr * (RF ? 4 : 2);
-    const char* g = a.gate ? (const char*)a.gate + row * a.ldg * (WF ? 4 : 2) : nullptr;
+    const char* g = GATE && a.gate ? (const char*)a.gate + row * a.ldg * (WF ? 4 : 2) : nullptr;
     Raw8<XF> v[CH];
     Raw8<RF> s[CH];
     Raw8<WF> gate[CH], weight[CH];
@@ -679,7 +683,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, MODE == kPlain && TPR <= 256
       if (i < n) {
         v[c] = load8<XF, EVEN>(x, i, n);
         if (a.residual) s[c] = load8<RF, EVEN>(r, i, n);
-        gate[c] = load_vec8<WF, EVEN>(g, 1.0f, i, n);
+        if (GATE) gate[c] = load_vec8<WF, EVEN>(g, 1.0f, i, n);
         weight[c] = load_vec8<WF, EVEN>(a.weight, 1.0f, i, n);
       }
     }
@@ -699,7 +703,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, MODE == kPlain && TPR <= 256
     for (int c = 0; c < CH; ++c) {
       const int i = (c * TPR + t) * 8;
       if (i < n) {
-        s[c] = join8<PLAIN, XF, RF, WF, EVEN>(a, v[c], s[c], gate[c], i, mean, rs);
+        s[c] = join8<PLAIN, GATE, XF, RF, WF, EVEN>(a, v[c], s[c], gate[c], i, mean, rs);
         if (a.residual_out) store8<RF, EVEN>((char*)a.residual_out + row * a.lds * (RF ? 4 : 2), i, n, s[c]);
       }
       s[c].renew();
@@ -892,7 +896,11 @@ hipError_t norm_kind(const NormArgs& a, hipStream_t s) {
   if (a.wf32) return norm_shape<XF, RF, kF32Weights>(a, s);
   if (a.n % 8) return norm_shape<XF, RF, kGeneral>(a, s);
   const bool plain = !a.layer && !a.bias && a.short_join;
-  return plain ? norm_shape<XF, RF, kPlain>(a, s) : norm_shape<XF, RF, kEven>(a, s);
+  if (!plain) return norm_shape<XF, RF, kEven>(a, s);
+  if constexpr (!XF) {
+    if (a.gate) return norm_shape<XF, RF, kPlainGate>(a, s);
+  }
+  return norm_shape<XF, RF, kPlain>(a, s);
 }
 
 template <bool YF, bool EVEN>
