@@ -7,7 +7,7 @@ import torch
 
 import quantized_dequant_gemm_amd as q
 from tests import gpu_helpers as H
-from tests.test_gpu_lora import Group, _ptr
+from tests.test_gpu_lora import Group, Pool, _ptr, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +130,33 @@ def test_infinities_and_nan_in_b(qdg, path, f32, rank):
         b[5] = np.inf
         got = _lora(path, np.array([first]), np.ones((rank, 1)), b, np.zeros(n), f32)
         np.testing.assert_array_equal(got[5], result)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("rank", [16, 28, 64])
+def test_several_units_of_columns_a_workgroup(qdg, f32, rank):
+    """So many blocks and columns that a workgroup of the kernel for many rows walks several units of B, one of them with
+    an infinity and one with a NaN: only their columns change."""
+    rng = np.random.default_rng(rank)
+    M, n, k, E, bm = 2048, 2100, 4200, 3, 64
+    pool = Pool(rng, n, k, rank, E, scales=False)
+    ids = rng.integers(0, E, M).astype(np.int32)
+    _run(rng, pool, ids, bm, f32)
+    g = Group(ids, E, bm)
+    x = _bf16(rng.standard_normal((M, k)))
+    cfg = q.lora(n, k, rank, num_adapters=E, otype=q.QDG_O_F32 if f32 else q.QDG_O_BF16)
+    nbytes = q.qdg_lora_workspace(cfg, M, bm)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    got = []
+    for bad in (False, True):
+        if bad:
+            pool.dB[1, 1900, rank - 1], pool.dB[2, 700, 0] = float("inf"), float("nan")
+        y = torch.zeros((M, n), dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+        q.qdg_lora(cfg, x.data_ptr(), pool.dA.data_ptr(), pool.dB.data_ptr(), None, None, *g.args(), y.data_ptr(),
+                   ws.data_ptr(), nbytes, q.current_stream())
+        torch.cuda.synchronize()
+        got.append(y)
+    first, second = torch.from_numpy(ids == 1).cuda(), torch.from_numpy(ids == 2).cuda()
+    assert torch.isinf(got[1][first, 1900]).all() and torch.isnan(got[1][second, 700]).all()
+    got[1][first, 1900], got[1][second, 700] = got[0][first, 1900], got[0][second, 700]
+    assert torch.equal(got[0], got[1])
