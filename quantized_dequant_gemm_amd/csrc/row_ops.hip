@@ -558,18 +558,21 @@ __device__ __forceinline__ Raw8<RF> join8(const NormArgs& a, const Raw8<XF>& x, 
     }
     const double offset = a.post_weight ? (double)a.weight_offset : 0.0;
     const int rest = n - i;
-    float v[2];
+    float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       double d = (double)x[j];
       if (!PLAIN) d = (d - mean) * rs * ((double)w[j] + offset) + (double)b[j];
       d = __builtin_fma((double)scale, (double)r[j], d * (double)g[j]);
-      v[j & 1] = EVEN || j < rest ? (float)d : 0.f;
-      if (j & 1) {
-        put(j >> 1, v[0], v[1]);
-        one_at_a_time();
-      }
+      v[j] = (float)d;
+      if (j & 1) one_at_a_time();
     }
+    if (!EVEN && rest < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < rest ? v[j] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) put(j, v[2 * j], v[2 * j + 1]);
   }
   return s;
 }
