@@ -702,7 +702,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kWideWaves<
   __shared__ u32x4_t terms[4 * STEPS * kTerms];
   __shared__ u32x4_t lds[kSides][STEPS * kBStep / 16];
   constexpr int kP = YF ? 2 : 1, kE = YF ? 4 : 8;  // pieces of a lane's row, elements a piece
-  constexpr int kB = YF ? 8 : STEPS == 2 ? 2 : 4;  // column tiles at a time, as many as registers hold
+  constexpr int kB = YF ? 8 : STEPS <= 2 ? 2 : 4;  // column tiles at a time, as many as registers hold
   const int group = tile_group(a, 4);
   if (group < 0 || group * 4 >= tiles) return;
   const int tile0 = group * 4;
@@ -714,9 +714,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kWideWaves<
   int row[4];  // of 4 c + i; -1: padding
 #pragma unroll
   for (int i = 0; i < 4; ++i) row[i] = row_at(a, (tile0 + wave) * 16 + 4 * c + i);
-  // a row's place in Y, worked out anew each time: 64 bits of each row would be registers
+  // a row's place in Y; worked out anew each time where 64 bits of each row would
+  // be registers that spill (rank 32 26.3 against 26.7 us; rank 16 114 against 112.5)
   auto place = [&](int i) {
-    asm volatile("" : "+v"(row[i]));
+    if constexpr (STEPS > 1 && !YF) asm volatile("" : "+v"(row[i]));
     return (int64_t)row[i] * a.ldy + (YF ? 4 : 8) * q;
   };
   // B: a thread has eight ranks of a column in each step
