@@ -108,7 +108,8 @@ __device__ __forceinline__ int row_at(const LoraArgs& a, int i) {
 // neighbouring lanes would be in 16 different rows, a lane a clock on the way
 // in: 2048 rows, k = 14336 took 51 us so, 41 by lines.) A wave turns them in LDS of its own, chunk x of row q at
 // place x ^ (q % 8), so that eight neighbouring lanes meet eight places on both
-// sides (x ^ (q / 2), sixteen places, is as fast).
+// sides (x ^ (q / 2), sixteen places, is as fast: 2048 rows of rank 64, k = 14336
+// 39.5 us both, 512 rows of rank 16 11.4 against 11.3 to 11.5).
 constexpr int kTileBytes = 2048;
 
 // The rows of X that a lane reads. Padding comes last in a tile, so a tile with
@@ -225,10 +226,10 @@ __device__ __forceinline__ void inner_sums(const LoraArgs& a, const uint16_t* co
 // T of MT x 16 rows and NT x 16 columns (ranks of one or several slices):
 // workgroup = (rows, columns, K part), its four waves share the K part. What
 // padding rows read is not used. Two operand tiles of loads a step for each MFMA
-// pair: the way in bounds it, not the matrix cores. 4096 rows, k = 4096, two
-// slices of 16 ranks 15.6 us (33 MB of X once: 2.2 TB/s), 2048 rows, k = 14336, 64
-// ranks 21.5 us (63 MB from memory, 2.9 TB/s; each adapter's A again for each 32
-// rows, from L2).
+// pair: the way in bounds it, not the matrix cores. In a kernel trace 4096 rows,
+// k = 4096, two slices of 16 ranks take 16 us at least, 19 at the median (33 MB of
+// X once: 1.7 to 2.1 TB/s), 2048 rows, k = 14336, 64 ranks 22 and 29 (63 MB from
+// memory, 2.2 to 2.9 TB/s; each adapter's A again for each 32 rows, from L2).
 template <int MT, int NT, bool ODD>
 __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int tiles, int wave_steps) {
   __shared__ u32x4_t lds[4 * (MT + NT) * kTileBytes / 16 > 4 * MT * NT * 64 ? 4 * (MT + NT) * kTileBytes / 16 : 4 * MT * NT * 64];
@@ -282,6 +283,9 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a, int tiles, i
 __device__ __forceinline__ uint32_t head_pair(float lo, float hi) {
   return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
 }
+__device__ __forceinline__ u32x4_t heads(const float (&v)[8]) {
+  return u32x4_t{head_pair(v[0], v[1]), head_pair(v[2], v[3]), head_pair(v[4], v[5]), head_pair(v[6], v[7])};
+}
 __device__ __forceinline__ float tail(float t) {
   return t - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, t) & 0xFFFF0000u);
 }
@@ -294,13 +298,13 @@ __device__ __forceinline__ float tail(float t) {
 // with nothing left.
 constexpr int kTerms = 97;
 __device__ __forceinline__ void store_terms(u32x4_t* t, int l, float (&v)[8]) {
-  t[l] = u32x4_t{head_pair(v[0], v[1]), head_pair(v[2], v[3]), head_pair(v[4], v[5]), head_pair(v[6], v[7])};
+  t[l] = heads(v);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = fabsf(v[j]) < __builtin_inff() ? tail(v[j]) : 0.f;
-  t[32 + l] = u32x4_t{head_pair(v[0], v[1]), head_pair(v[2], v[3]), head_pair(v[4], v[5]), head_pair(v[6], v[7])};
+  t[32 + l] = heads(v);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = tail(v[j]);
-  t[64 + l] = u32x4_t{head_pair(v[0], v[1]), head_pair(v[2], v[3]), head_pair(v[4], v[5]), head_pair(v[6], v[7])};
+  t[64 + l] = heads(v);
   if (l == 0) t[96] = u32x4_t{0, 0, 0, 0};
 }
 __device__ __forceinline__ int third_place() {
@@ -526,8 +530,8 @@ __device__ __forceinline__ Columns columns_of(const LoraArgs& a, int chunk, int 
 
 // Y: workgroup = (MT x 16 rows, `span` units of 64 columns of one slice), a
 // wave takes every fourth unit. 250 rows of 12 adapters, rank 64, 4100 columns of
-// binary32 9.4 to 11 us (14 MB): a workgroup or two a CU, each the chain of
-// grouping, partials, terms, products, so latency bounds it.
+// binary32 10 to 11 us in a kernel trace (14 MB): a workgroup or two a CU, each the
+// chain of grouping, partials, terms, products, so latency bounds it.
 template <int MT, bool YF, bool ODD>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int tiles) {
   const int span = a.span;
@@ -593,8 +597,8 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int tiles) {
 // Every workgroup of a slice computes T anew: (16 NT + 16) k values of A and X,
 // most of them from the caches, in place of a second launch and the partials'
 // way through memory. The unit's B and Y are asked for before T is ready. One
-// row, k = n = 4096, rank 16 6.3 us: the chain of the grouping's loads, a wave's
-// 512 values of k and three joins; 64 rows of 48 adapters, 6144 columns 11.3 us
+// row, k = n = 4096, rank 16 6.8 us: the chain of the grouping's loads, a wave's
+// 512 values of k and three joins; 64 rows of 48 adapters, 6144 columns 11.4 us
 // (22 MB of A and B).
 constexpr int kFusedWaves = 8;
 template <int NT, bool YF, bool ODD>
@@ -685,17 +689,19 @@ __global__ __launch_bounds__(64 * kFusedWaves) void lora_fused_kernel(LoraArgs a
 // a lane of the result holds 16 bytes of a row and 16 neighbouring lanes 256
 // bytes in a line: Y comes and goes by whole lines. B's unit goes through LDS
 // for the four waves, [rank step][column][16 ranks], 16 bytes more every eight
-// columns (neighbours in different banks); the next unit's B and Y are on their
-// way meanwhile. 4096 rows, 28672 columns of bf16, rank 16 86 us (5.0 TB/s of Y
-// there and back: HBM); 2048 rows, rank 64, 4096 columns 13 us (39 MB, 3.0 TB/s:
-// two rounds of workgroups). Four waves a SIMD where 128 registers hold a step
-// (gate-up 104 -> 97 us), three with four steps of B on their way, two and no
+// columns (a third of the LDS cycles still conflict); the next unit's B and Y are
+// on their way meanwhile. In a kernel trace 4096 rows, 28672 columns of bf16, rank
+// 16 take 85 us at least, 100 at the median (433 MB of Y there and back and B: 4.3
+// to 5.1 TB/s, HBM), 2048 rows, rank 64, 4096 columns 15 and 17 (39 MB, 2.4 to 2.7
+// TB/s: two rounds of workgroups). Four waves a SIMD where 128 registers hold a
+// step (gate-up 104 -> 97 us), three with four steps of B on their way, two and no
 // more beside binary32 Y (gate-up of rank 16 195 against 204 us with three).
 constexpr int kWide = 128, kBStep = kWide * 32 + kWide / 8 * 16;
 template <int STEPS, bool YF>
 constexpr int kWideWaves = YF ? 2 : STEPS == 4 ? 3 : 4;
 template <int STEPS, bool YF, bool ODD>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kWideWaves<STEPS, YF>, YF ? 2 : 8))) void lora_wide_kernel(LoraArgs a, int tiles) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kWideWaves<STEPS, YF>, YF ? 2 : 8)))
+void lora_wide_kernel(LoraArgs a, int tiles) {
   const int span = a.span;
   // one side with four steps: 42 KB let a third workgroup in (4096 rows, rank 64 35.6 against 36.7 us)
   constexpr int kSides = STEPS == 4 ? 1 : 2;
@@ -799,7 +805,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kWideWaves<
         const u32x4_t tf = tt[lane], third = tt[third_place()];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const u32x4_t bf = *(const u32x4_t*)(bl + s * kBStep + (YF ? u / 4 * 8 * 272 + u % 4 * 32 : u * 32)), fin = finite_part(bf);
+          const u32x4_t bf = *(const u32x4_t*)(bl + s * kBStep + (YF ? u / 4 * 8 * 272 + u % 4 * 32 : u * 32));
+          const u32x4_t fin = finite_part(bf);
           acc[u] = mfma_bf16(tf, lane & 32 ? fin : bf, acc[u]);
           acc[u] = mfma_bf16(third, fin, acc[u]);
           __builtin_amdgcn_sched_barrier(0);  // one tile at a time: registers
@@ -854,16 +861,21 @@ void lora_choose(LoraArgs* a) {
   a->rank_pad = (a->rank + 15) / 16 * 16;
   const int nt = a->rank_pad / 16, groups = a->num_slices * nt;
   // One launch where T, anew for every 512 columns, costs less than the second
-  // launch and the partials: T takes 4.4 us and 0.5 us (16 ranks) or 0.85 us (32)
-  // for 1024 values of k while all workgroups run at once; two launches 6.5 to 8
-  // us in a graph, 2 more without. n = 4096: 1 row of rank 8, k = 1024 4.9 against
-  // 6.5, k = 4096 6.5 against 6.7; rank 32, k = 1024 6.3 against 7.2, k = 4096 8.8
-  // against 7.3; k = 14336, rank 8 12.3 against 8.3. Blocks of one tile, each its
-  // own adapter's, gain up to two workgroups a CU (64 rows of 48 adapters, 6144
-  // columns 11.4 against 15.4 us), larger blocks up to one (512 rows of 4
-  // adapters 13.0 against 10.7).
+  // launch and the partials, while all workgroups run at once. n = 4096, 1 row of
+  // rank 8: k = 1024 5.2 against 6.8 us, k = 4096 6.8 against 7.0, k = 14336 12.5
+  // against 8.5; rank 32: k = 1024 6.8 against 7.4, k = 2560 7.9 against 7.5, k =
+  // 4096 9.1 against 7.6. Larger blocks gain up to a workgroup a CU (200 rows of 2
+  // adapters, 2048 columns 7.5 against 9.3 us; 512 rows of 4, 4096 columns, which
+  // need 352, 13.6 against 10.8). Of blocks of one tile, each its own adapter's, two
+  // fit a CU up to 16 ranks and bf16 Y (64 rows of 48 adapters, 6144 columns 11.4
+  // against 12.2 us, 608 workgroups of k = 4096 12.6 against 14.1); of binary32 Y or
+  // more ranks one fits. Some blocks have no rows and leave at once: 344 at most are
+  // 256 with rows (k = 4096, binary32 9.1 against 10.3 us, 376 of them 14.7 against
+  // 11.1; rank 32, k = 2048 9.8 against 10.8, 13.5 against 11.5; from 450 on the two
+  // differ by up to 12 % either way, one launch ahead at a short k).
+  const int workgroups = a->block_m > 16 ? 256 : nt == 1 && !a->yf32 ? 640 : 352;
   a->fused = (nt + 1) * (int64_t)a->k <= 8192 && nt <= 2 &&
-             tiles * chunks_of(*a, kFusedWaves * kUnit) <= (a->block_m == 16 ? 640 : 256);
+             tiles * chunks_of(*a, kFusedWaves * kUnit) <= workgroups;
   // Parts of K: 512 workgroups (two a CU) where there is that much, each wave
   // with two steps of 64 at least.
   const int mt = groups > 2 && tiles_per_group(a->block_m) > 2 ? 2 : tiles_per_group(a->block_m);
@@ -871,11 +883,11 @@ void lora_choose(LoraArgs* a) {
   // Units of columns a workgroup: each adds up T anew, split * rank_pad * 256
   // bytes for 64 rows, beside 32 KB of a unit's Y there and back; so more units
   // the more there is to add up, while 256 workgroups are left, and more while
-  // 1024 are (4096 rows, rank 32, k = n = 4096: 30.5 us with one unit, 26.7 so). Few
+  // 1024 are (4096 rows, rank 32, k = n = 4096: 29.0 us with one unit, 26.3 so). Few
   // rows: a unit for each of four waves, more while 768 workgroups are left (16
   // rows of as many adapters, 28672 columns: 10.6 us with one unit, 9.1 so).
   // 64 rows at once, Y by whole lines, from 64-row blocks on: 4096 rows of rank
-  // 16, k = 4096, n = 28672 144 against 112 us, rank 64, n = 4096 40 against 35
+  // 16, k = 4096, n = 28672 147 against 113 us, rank 64, n = 4096 41 against 36
   // (more than 64 ranks are more registers than hold the next unit's B and Y).
   a->wide = tiles_per_group(a->block_m) == 4 && a->rank_pad <= 64;
   if (a->wide) {
