@@ -439,8 +439,9 @@ constexpr uint32_t kMiddle = (uint32_t)(2 * ULPS) << 16 | 0xFFFFu;
 // (without an instance of its own 4096 x 4096 with fp8 codes alone takes 29.9 us
 // instead of 26.8). kEven: anything else
 // with bf16 weights in rows of whole chunks. kGeneral: bf16 weights, a cut last
-// chunk. kF32Weights: any row (one more instance for whole chunks would bring
-// 4096 x 4096 from 48.8 to 47.3 us and 4096 x 8192 layer from 109 to 114).
+// chunk. kF32Weights: any row (4096 x 4096 42.0 us, 33.1 with bf16 weights; with a
+// bias 46.2; one more instance for whole chunks with a bias brought 4096 x 4096
+// from 48.8 to 47.3 us and 4096 x 8192 layer from 109 to 114).
 enum { kPlain, kPlainGate, kEven, kGeneral, kF32Weights };
 
 // 1 / sqrt(x): v_rsq_f64 (2^-14 or better) and three steps of Newton's
@@ -654,9 +655,8 @@ __device__ __forceinline__ Raw8<false> norm8(const NormArgs& a, const Raw8<RF>& 
 
 // One pass over a row in registers: the join, its sum of squares (and sum), the
 // normed values, the codes' statistics, rows and codes. 4096 x 4096 bf16 with
-// rows and int8 zp codes 33 us (4.6 TB/s, what a large copy reaches), 8192 x
-// 8192 layer in binary32 with 4-bit codes 145 us (4.9), where HBM is what bounds
-// it; 333 x 7168 norms on both sides 13.2 us (2.7 TB/s): one workgroup or two a
+// rows and int8 zp codes 33 us (4.6 TB/s), 8192 x 8192 layer in binary32 with
+// 4-bit codes 146 us (4.8), where HBM is what bounds it; 333 x 7168 norms on both sides 13.2 us (2.7 TB/s): one workgroup or two a
 // CU, each a chain of load, two sums with a barrier, stores; 1 x 4096 3.8 us in a
 // graph. Four waves a SIMD are 128 registers; kPlain in 256 threads has five in
 // 96 (4096 x 4096 with fp8 codes alone 26.8 against 28.1 us, with a binary32
@@ -829,8 +829,9 @@ __device__ __forceinline__ Raw8<false> gated8(const Raw8<YF>& g, const Raw8<YF>&
 // A piece of TPR * CH * 8 columns of a row for each blockIdx.y: one for int8
 // codes, which need the row's largest value. 4096 x 14336 with fp8 codes 70.5 us
 // (4.2 TB/s): HBM, and some 40 vector instructions for each 64 values beside it,
-// two of them transcendental; with int8 codes 66 us. Without the bound of four
-// waves a SIMD the int8 instances take more registers and one row a CU (103 us).
+// two of them transcendental; with int8 codes 68 us (28 bytes a lane spilled).
+// Without the bound of four waves a SIMD the int8 instances take more registers
+// and one row a CU (103 us). GELU 78 and 75 us, binary32 Y 106.
 template <int TPR, int CH, bool YF, bool EVEN>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void gated_kernel(GatedArgs a) {
   __shared__ Buffers buf;
