@@ -755,13 +755,13 @@ qdg_status qdg_gated_act(const qdg_gated_config* cfg, const void* Y, int64_t M, 
    to 0 .. rank; entries of A and B behind an adapter's rank may hold anything)
    or NULL (all rank); scales f32 [num_adapters] or NULL (all 1); Y [M][n] of
    otype BF16 or F32, row stride ldy. All aligned to their elements.
-   Products of bf16 numbers are exact in binary32 and are added there; the
-   inner sums enter the second product, scaled, with all 24 bits of their
-   significand (of those below 2^-109 only what is above 2^-133); the sum joins
-   Y in binary32 and is rounded once to otype. Infinities and NaN in X, A and
-   B go the way of IEEE arithmetic (ranks behind an adapter's own do not count). Results do not depend on other rows'
-   values, but their last bits may on M and the grouping (the order of the inner
-   sums).
+   Products of bf16 numbers are exact in binary32, where it holds them, and are
+   added there; the inner sums enter the second product, scaled, with all 24
+   bits of their significand (of those below 2^-109 only what is above 2^-133);
+   the sum joins Y in binary32 and is rounded once to otype. Infinities and NaN
+   in X, A and B go the way of IEEE arithmetic (ranks behind an adapter's own do
+   not count). Results do not depend on other rows' values, but their last bits
+   may on M and the grouping (the order of the inner sums).
    n, k in [1, 2^20]; rank 1..256; num_slices 1..4, slice_end ascending, the
    last one n; num_adapters 1..1024; M in [0, 2^20] (0 enqueues nothing);
    block_m 16, 32, 64 or 128: the smaller while adapters hold few rows each
